@@ -83,6 +83,7 @@ typedef struct CUstream_st* qe_stream_t;
 /* Activation dtypes. */
 #define QE_F32 0
 #define QE_BF16 1
+#define QE_F16 2 /* attn_* and token_sample only */
 
 /* One packed matrix (device pointers). */
 typedef struct {
@@ -406,6 +407,140 @@ QE_API void qe_trace_fused(void* dev_buf);
  * finished.  The arithmetic is fp32 (the pages use single-precision BLAS). */
 QE_API int gdn_decode_step(int n_heads, int dk, int dv, float* state, const float* q, const float* k,
                            const float* v, const float* alpha, const float* beta, float* out, qe_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Attention of a decode step over a paged cache: the token mixer of the
+ * model's 15 full-attention layers, which stand where gdn_decode_step stands
+ * in the other 45 (lilting.ch "Flash-MoE", section "Metal Compute Shaders":
+ * GPU attention, Q K^T, softmax, scores V).  The pages name the three products
+ * only; grouped heads, pages, the shared prefix and the rotation are this
+ * library's.
+ *
+ * The cache of one layer: n_pages pages of page_size tokens for each of n_kv
+ * key heads, key (page p, head h, token j) at
+ *   k + p * k_page_stride + (h * page_size + j) * head_dim      (elements)
+ * and the value alike from v.  bf16 or fp16; k, v 16-byte aligned and the page
+ * strides a multiple of 8 elements, at least n_kv * page_size * head_dim.
+ * head_dim 64, 128 or 256; 1 <= page_size <= 65536; n_kv <= 1024. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t k_page_stride; /* elements */
+  int64_t v_page_stride; /* elements */
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t n_kv;
+  int32_t head_dim;
+  int32_t dtype; /* QE_BF16 or QE_F16 */
+  int32_t reserved;
+} qe_kv_cache;
+
+/* Rotary positions: pair i of a head turns by the angle
+ *   pos[axis(i)][t] * inv_freq[i],    i = 0 .. rotary_dim / 2 - 1,
+ * as (a, b) -> (a cos - b sin, b cos + a sin); the elements from rotary_dim on
+ * are copied.  adjacent != 0: pair i is elements 2i and 2i + 1, else i and
+ * i + rotary_dim / 2.  pair_axis (HOST array [rotary_dim / 2], copied by the
+ * call, NULL = axis 0 for all) says which of the n_axes positions of a token
+ * (1 to 4: one for text; time, height and width for images and video) turns
+ * pair i, in any order.  rotary_dim is a multiple of 16 and at most head_dim.
+ * inv_freq fp32 [rotary_dim / 2] device.  The angle is formed and reduced in
+ * fp64, so far positions keep fp32 accuracy. */
+typedef struct {
+  const float* inv_freq;
+  const uint8_t* pair_axis;
+  int32_t rotary_dim;
+  int32_t n_axes;
+  int32_t adjacent;
+  int32_t reserved;
+} qe_rope;
+
+/* Rotate q and k of T tokens and append k and v to the cache.
+ *   q [T][n_q][head_dim], k and v [T][n_kv][head_dim] device, in_dtype QE_F32,
+ *     QE_BF16 or QE_F16; q_stride, k_stride, v_stride: elements from one token
+ *     to the next (a fused projection's output can be passed as it is), a
+ *     multiple of 8; all 16-byte aligned.  q may be NULL with n_q = 0.
+ *   q_out [T][n_q][head_dim] device, the cache's dtype, q_out_stride as above.
+ *     It may be q itself (same dtype and stride); otherwise it must not
+ *     overlap q, k or v.
+ *   rope NULL: nothing is rotated (q_out is q in the cache's dtype).
+ *   pos int32 [n_axes][T] device: positions for the rotation, NULL = kv_pos on
+ *     every axis.
+ *   kv_pos int32 [T] device: place of token t among its sequence's own tokens;
+ *     negative marks a padding row, of which nothing is read or written.
+ *   seq int32 [T] device: row of `table` of token t, NULL = t.
+ *   table int32 [n_seq][table_stride] device: page of tokens
+ *     [j * page_size, (j + 1) * page_size) of a sequence at column j.
+ * Arithmetic fp32; each element is rounded once, to the cache's dtype.  A
+ * token whose seq, column or page is out of range is not appended (its q is
+ * still rotated) and QE_ERR_INVALID_ARG is recorded in the workspace.  Two
+ * tokens of one call must not name the same place.  dev_ws: any workspace
+ * with a control block (256 bytes or more).  One launch. */
+QE_API int attn_kv_append(const qe_kv_cache* cache, const qe_rope* rope, int T, int n_q, const void* q, const void* k,
+                          const void* v, int in_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride, void* q_out,
+                          int64_t q_out_stride, const int32_t* pos, const int32_t* kv_pos, const int32_t* seq,
+                          const int32_t* table, int n_seq, int table_stride, void* dev_ws, size_t ws_bytes,
+                          qe_stream_t stream);
+
+/* Bytes of device workspace attn_decode_step needs for B rows of n_q heads on
+ * the current device, whatever the lengths.  0 for an invalid shape. */
+QE_API size_t attn_workspace_bytes(const qe_kv_cache* cache, int n_q, int B);
+
+/* Attention of B rows, one query token each, over a prefix that all of them
+ * share, followed by each row's own tokens:
+ *   out[b,i] = sum_j p_j v_j,  p = softmax_j(scale q[b,i] . k_j),
+ * j over the prefix_len tokens of the pages prefix_pages[0 ..], then the
+ * kv_len[b] tokens of the pages table[b][0 ..]; head i reads key head
+ * i / (n_q / n_kv).  The prefix is read once for the whole batch.
+ *   q, out [B][n_q][head_dim] device, the cache's dtype, 16-byte aligned, not
+ *     overlapping; q_stride, out_stride: elements from row to row, a multiple
+ *     of 8.
+ *   prefix_pages int32 device [ceil(prefix_len / page_size)], NULL with
+ *     prefix_len = 0.  prefix_len is a host value (a captured graph keeps it).
+ *   kv_len int32 [B] device; table int32 [B][table_stride] device.  kv_len 0:
+ *     the prefix alone; with no prefix either, out is 0 and lse -inf.
+ *     Negative: a padding row, whose out and lse are left as they were.
+ *   lse fp32 [B][n_q] device or NULL: ln sum_j exp(scale q . k_j).
+ * Several query tokens of one sequence are several rows with the same pages
+ * and kv_len one apart.  n_q % n_kv == 0, n_q <= 1024, B <= 4096,
+ * table_stride * page_size and prefix_len < 2^30.  Scores, softmax statistics
+ * and sums are fp32; the softmax numerators are rounded to the cache's dtype
+ * for the product with v.  A kv_len beyond the table is cut to it, a key on a
+ * page out of range counts as masked, and either records QE_ERR_INVALID_ARG in
+ * the workspace.  The result does not depend on the order in which the GPU
+ * runs the parts.  Calls that share a workspace must be ordered on the device. */
+QE_API int attn_decode_step(const qe_kv_cache* cache, int B, int n_q, const void* q, int64_t q_stride,
+                            const int32_t* prefix_pages, int prefix_len, const int32_t* table, int table_stride,
+                            const int32_t* kv_len, float scale, void* out, int64_t out_stride, float* lse,
+                            void* dev_ws, size_t ws_bytes, qe_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * The next token of B rows from their logits and given uniform numbers: the
+ * step after the last layer (the pages' engine samples on the CPU).  Row b,
+ * with x_max its largest logit and e_i = exp((x_i - x_max) / temperature[b]):
+ *   1. candidates in descending order of x, ties to the lower index;
+ *   2. the first top_k[b] of them (<= 0 or >= V: all);
+ *   3. of those, the shortest run whose mass reaches top_p[b] of theirs (at
+ *      least one; >= 1: all);
+ *   4. of those, e_i >= min_p[b] (the largest has e = 1; <= 0: all);
+ *   5. token[b] = the first index i, ascending, at which the running sum of
+ *      the kept e exceeds u[b] times their total.
+ * temperature[b] <= 0 or NaN: the largest logit (lowest index), logprob 0.  A
+ * logit of -inf or NaN is never chosen; a row with no other gives token -1
+ * and logprob -inf.  If the largest is +inf, only the logits of +inf weigh.
+ * u <= 0 or NaN gives the first kept token, u >= 1 the last.
+ *   logits [B][V] device, dtype QE_F32, QE_BF16 or QE_F16, stride elements
+ *     from row to row (any alignment of its element size).
+ *   temperature, top_p, min_p fp32 [B] and top_k int32 [B] device, each NULL
+ *     for "as 1, 1, 0, 0"; u fp32 [B] device.
+ *   token int32 [B] device; logprob fp32 [B] device or NULL: ln of the chosen
+ *     token's probability among the kept ones.
+ * Weights are fp64, rounded to multiples of 2^-S of the largest, S =
+ * min(46, 62 - ceil(log2 V)); all sums are exact integers, so a row's token does
+ * not depend on the batch it is in, nor on the order of any sum.  1 <= V <=
+ * 524288; one launch, no workspace. */
+QE_API int token_sample(const void* logits, int dtype, int B, int V, int64_t stride, const float* temperature,
+                        const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* token,
+                        float* logprob, qe_stream_t stream);
 
 #ifdef __cplusplus
 }

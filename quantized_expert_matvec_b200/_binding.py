@@ -20,16 +20,18 @@ QE_ERR_TIMEOUT = -4
 QE_ERR_OOM = -5
 QE_F32 = 0
 QE_BF16 = 1
+QE_F16 = 2
 
 __all__ = [
     "LIB_PATH", "lib", "QEError", "Cfg", "QMat", "Expert", "Layer", "ExpertPool",
     "QE_OK", "QE_ERR_INVALID_ARG", "QE_ERR_UNSUPPORTED", "QE_ERR_CUDA", "QE_ERR_TIMEOUT", "QE_ERR_OOM",
-    "QE_F32", "QE_BF16",
+    "QE_F32", "QE_BF16", "QE_F16",
     "qe_last_error", "qe_version", "qe_expert_bytes", "qe_pool_table", "qe_workspace_bytes",
     "qe_workspace_init", "qe_workspace_status", "qe_set_wait_budget_ns", "qe_test_skip_arrival", "qe_trace_fused",
     "moe_route", "moe_expert_ffn_q4", "moe_expert_ffn_q2", "moe_expert_ffn_mixed", "moe_combine",
     "moe_layer_step", "moe_layer_step_noalloc", "moe_layer_step_host", "workspace", "Tier", "TierDesc",
     "gdn_decode_step",
+    "KVCache", "Rope", "attn_workspace_bytes", "attn_workspace", "attn_kv_append", "attn_decode_step", "token_sample",
 ]
 
 
@@ -67,7 +69,22 @@ class TierDesc(ctypes.Structure):
                 ("cold_host", ctypes.POINTER(ctypes.c_void_p)), ("cache_bytes", ctypes.c_size_t)]
 
 
+class KVCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_page_stride", ctypes.c_int64),
+                ("v_page_stride", ctypes.c_int64), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("pair_axis", ctypes.POINTER(ctypes.c_uint8)),
+                ("rotary_dim", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("adjacent", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 assert ctypes.sizeof(TierDesc) == 56
+assert ctypes.sizeof(KVCacheDesc) == 56
+assert ctypes.sizeof(RopeDesc) == 32
 
 
 assert ctypes.sizeof(Expert) == 96
@@ -78,7 +95,7 @@ def _load():
         raise ImportError(f"{LIB_PATH} is missing: build it with quantized_expert_matvec_b200/build.py "
                           "(or __graft_entry__.build()); there is no CPU fallback")
     L = ctypes.CDLL(LIB_PATH)
-    vp, i32, sz, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+    vp, i32, i64, sz, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     P = ctypes.POINTER
     sigs = {
         "qe_last_error": (ctypes.c_char_p, []),
@@ -106,6 +123,11 @@ def _load():
         "qe_tier_slots": (i32, [vp]),
         "qe_tier_destroy": (None, [vp]),
         "gdn_decode_step": (i32, [i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "attn_kv_append": (i32, [P(KVCacheDesc), P(RopeDesc), i32, i32, vp, vp, vp, i32, i64, i64, i64, vp, i64, vp, vp,
+                                 vp, vp, i32, i32, vp, sz, vp]),
+        "attn_workspace_bytes": (sz, [P(KVCacheDesc), i32, i32]),
+        "attn_decode_step": (i32, [P(KVCacheDesc), i32, i32, vp, i64, vp, i32, vp, i32, vp, f, vp, i64, vp, vp, sz, vp]),
+        "token_sample": (i32, [vp, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -369,3 +391,181 @@ def gdn_decode_step(state, q, k, v, alpha, beta, out, stream=None):
             raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
     _check(lib.gdn_decode_step(nh, dk, dv, _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta),
                                _ptr(out), _stream(stream)))
+
+
+def _code(dtype):
+    import torch
+    try:
+        return {torch.float32: QE_F32, torch.bfloat16: QE_BF16, torch.float16: QE_F16}[dtype]
+    except KeyError:
+        raise ValueError(f"expected float32, bfloat16 or float16, got {dtype}") from None
+
+
+def _here(name, t, dtype=None, shape=None, dev=None):
+    """Data pointer of a CUDA tensor of the current device, after its dtype and
+    shape were checked; its strides are the caller's matter."""
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    return t.data_ptr()
+
+
+def _vec(name, t, dtype, shape, dev):
+    """As _here, for an optional dense tensor."""
+    if t is None:
+        return None
+    p = _here(name, t, dtype, shape, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return p
+
+
+def _heads(name, t, dtype, heads, dim, dev):
+    """Pointer and token stride of [T, heads, dim] with dense heads."""
+    p = _here(name, t, dtype, (t.shape[0], heads, dim), dev)
+    s = t.stride()
+    if (heads > 1 and s[1] != dim) or s[2] != 1:
+        raise ValueError(f"the heads of {name} must be dense")
+    return p, s[0]
+
+
+class KVCache:
+    """The paged cache of one layer over the caller's tensors: k and v
+    [n_pages, n_kv, page_size, head_dim], bfloat16 or float16, each page dense
+    (pages may be further apart: a slice over the layers of a larger pool)."""
+
+    def __init__(self, k, v):
+        import torch
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must be [n_pages, n_kv, page_size, head_dim] of one dtype and device")
+        if not k.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        if k.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"the cache is bfloat16 or float16, got {k.dtype}")
+        n, h, p, d = (int(x) for x in k.shape)
+        for name, t in (("k", k), ("v", v)):
+            if n and not t[0].is_contiguous():
+                raise ValueError(f"the pages of {name} must be dense")
+        page = h * p * d
+        self.k, self.v, self.dtype = k, v, k.dtype
+        self.n_kv, self.page_size, self.head_dim = h, p, d
+        self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), k.stride(0) if n > 1 else page, v.stride(0) if n > 1 else page,
+                                n, p, h, d, _code(k.dtype), 0)
+        self._ref = ctypes.byref(self.desc)
+
+
+class Rope:
+    """Rotary positions: inv_freq float32 CUDA [rotary_dim / 2]; pair_axis, the
+    position axis of each pair (None: axis 0); adjacent pairs (2i, 2i + 1)
+    instead of (i, i + rotary_dim / 2)."""
+
+    def __init__(self, inv_freq, pair_axis=None, adjacent=False, n_axes=None):
+        import torch
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not inv_freq.is_cuda:
+            raise ValueError("inv_freq must be a dense float32 CUDA vector")
+        n = inv_freq.numel()
+        self.inv_freq, axes = inv_freq, None
+        if pair_axis is not None:
+            axes = [int(i) for i in pair_axis]
+            if len(axes) != n or min(axes, default=0) < 0 or max(axes, default=0) > 3:
+                raise ValueError(f"pair_axis must name one of at most four axes for each of the {n} pairs")
+        self.n_axes = n_axes if n_axes is not None else (max(axes, default=0) + 1 if axes else 1)
+        self._axes = (ctypes.c_uint8 * n)(*axes) if axes else None
+        self.desc = RopeDesc(inv_freq.data_ptr(), ctypes.cast(self._axes, ctypes.POINTER(ctypes.c_uint8)) if axes else None,
+                             2 * n, self.n_axes, 1 if adjacent else 0, 0)
+        self._ref = ctypes.byref(self.desc)
+
+
+def attn_workspace_bytes(cache: KVCache, n_q: int, B: int) -> int:
+    n = int(lib.attn_workspace_bytes(cache._ref, n_q, B))
+    if n == 0:
+        raise QEError(QE_ERR_INVALID_ARG, qe_last_error())
+    return n
+
+
+def attn_workspace(cache: KVCache, n_q: int, B: int):
+    """Allocate (through torch) and zero a workspace for attn_decode_step with
+    B rows of n_q heads; it serves attn_kv_append too."""
+    import torch
+    ws = torch.empty(attn_workspace_bytes(cache, n_q, B), dtype=torch.uint8, device=cache.k.device)
+    qe_workspace_init(ws)
+    return ws
+
+
+def attn_kv_append(cache: KVCache, q, k, v, table, kv_pos, q_out=None, rope: Rope | None = None, pos=None, seq=None,
+                   ws=None, stream=None):
+    """Rotate q [T, n_q, head_dim] into q_out and append k, v [T, n_kv, head_dim]
+    to the cache, token t at place kv_pos[t] (int32; negative: padding) of the
+    sequence whose pages are table[seq[t]] (int32 [n_seq, columns]; seq None:
+    t).  pos int32 [n_axes, T] are the rotation's positions (None: kv_pos).  q may
+    be None; q_out may be q itself where the dtypes agree."""
+    import torch
+    dev, i32, D = torch.cuda.current_device(), torch.int32, cache.head_dim
+    T = k.shape[0]
+    _here("cache", cache.k, dev=dev)
+    kp, ks = _heads("k", k, None, cache.n_kv, D, dev)
+    vp, vs = _heads("v", v, k.dtype, cache.n_kv, D, dev)
+    n_q, qp, qs, op, os_ = 0, None, 0, None, 0
+    if q is not None:
+        n_q = q.shape[1]
+        qp, qs = _heads("q", q, k.dtype, n_q, D, dev)
+        op, os_ = _heads("q_out", q_out, cache.dtype, n_q, D, dev)
+    if v.shape[0] != T or (q is not None and (q.shape[0] != T or q_out.shape[0] != T)):
+        raise ValueError("q, k, v and q_out must have the same number of tokens")
+    if table.dim() != 2:
+        raise ValueError("table must be [n_seq, columns]")
+    if rope is not None:
+        _here("inv_freq", rope.inv_freq, dev=dev)
+    _check(lib.attn_kv_append(cache._ref, rope._ref if rope is not None else None, T, n_q, qp, kp, vp, _code(k.dtype),
+                              qs, ks, vs, op, os_,
+                              _vec("pos", pos, i32, (rope.n_axes if rope is not None else 1, T), dev),
+                              _vec("kv_pos", kv_pos, i32, (T,), dev), _vec("seq", seq, i32, (T,), dev),
+                              _vec("table", table, i32, None, dev), table.shape[0], table.shape[1],
+                              _vec("ws", ws, torch.uint8, None, dev), ws.numel(), _stream(stream)))
+
+
+def attn_decode_step(cache: KVCache, q, out, table, kv_len, prefix_pages=None, prefix_len=0, scale=None, lse=None,
+                     ws=None, stream=None):
+    """Attention of B rows q [B, n_q, head_dim] over the prefix_len tokens on
+    prefix_pages (int32), shared by all rows, and each row's kv_len[b] own
+    tokens on table[b] (int32 [B, columns]; kv_len negative: a padding row, left
+    as it was), into out.  scale defaults to head_dim ** -0.5; lse float32
+    [B, n_q] receives the logarithm of the softmax's denominator."""
+    import torch
+    dev, i32, D = torch.cuda.current_device(), torch.int32, cache.head_dim
+    B, n_q = q.shape[0], q.shape[1]
+    _here("cache", cache.k, dev=dev)
+    qp, qs = _heads("q", q, cache.dtype, n_q, D, dev)
+    op, os_ = _heads("out", out, cache.dtype, n_q, D, dev)
+    if out.shape[0] != B or table.dim() != 2 or table.shape[0] != B:
+        raise ValueError("q, out and table must have the same number of rows")
+    if prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() * cache.page_size < prefix_len):
+        raise ValueError("prefix_pages must hold prefix_len tokens")
+    _check(lib.attn_decode_step(cache._ref, B, n_q, qp, qs, _vec("prefix_pages", prefix_pages, i32, None, dev),
+                                prefix_len, _vec("table", table, i32, None, dev), table.shape[1],
+                                _vec("kv_len", kv_len, i32, (B,), dev), D ** -0.5 if scale is None else scale, op, os_,
+                                _vec("lse", lse, torch.float32, (B, n_q), dev), _vec("ws", ws, torch.uint8, None, dev),
+                                ws.numel(), _stream(stream)))
+
+
+def token_sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None, stream=None):
+    """The next token of each row of logits [B, V] from the uniform numbers u
+    (float32 [B]) into token (int32 [B]): temperature, top_p, min_p float32 [B]
+    and top_k int32 [B], each None for "off"; logprob float32 [B] receives the
+    logarithm of the chosen token's probability among those kept."""
+    import torch
+    dev, i32, f32 = torch.cuda.current_device(), torch.int32, torch.float32
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be [B, V] with dense rows")
+    B, V = logits.shape
+    n = (B,)
+    _check(lib.token_sample(_here("logits", logits, dev=dev), _code(logits.dtype), B, V, logits.stride(0),
+                            _vec("temperature", temperature, f32, n, dev), _vec("top_k", top_k, i32, n, dev),
+                            _vec("top_p", top_p, f32, n, dev), _vec("min_p", min_p, f32, n, dev),
+                            _vec("u", u, f32, n, dev), _vec("token", token, i32, n, dev),
+                            _vec("logprob", logprob, f32, n, dev), _stream(stream)))

@@ -1,0 +1,608 @@
+// qe_sample.cu -- the next token of each row from its logits and a given
+// uniform number: temperature, top-k, top-p and min-p.
+//
+// With x_max the row's largest logit, e_i = exp((x_i - x_max) / temperature).
+// The candidates in descending order of x (ties: lower index first) are cut to
+// the first top_k; of those to the shortest run whose mass reaches top_p of
+// theirs; of those to e_i >= min_p.  The token is the first index i (ascending)
+// at which the running sum of the kept e exceeds u times their total.
+//
+// A token is a whole number: it changes when a running sum crosses u times the
+// total, so the sums have to be the same whoever adds them up in whichever
+// order.  Each e_i is computed in fp64 and rounded to a multiple of 2^-S,
+// S = 62 - ceil(log2 V) (at most 46), and the sums are exact 64-bit integers.
+// The rounding moves a border by at most V 2^-(S+1) of the largest weight; a
+// weight below 2^-(S+1) of it counts as 0.
+//
+// The row is read once.  A cluster of CTAs shares it, each holding a run of the
+// row as stored in its shared memory; a thread owns an odd number of
+// consecutive 16-byte pieces, so that threads are in index order (which the
+// running sums need) and their 16-byte reads fall on different banks.  The
+// cuts need no sort: a histogram of 2048 bins over x_max - x (7 mantissa bits of 16
+// binades), summed over the cluster through distributed shared memory, gives
+// the bin in which the k-th token or the top_p mass lies; further histograms
+// over the bin's order-preserving keys, 11 bits at a time, give the key itself.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "qe_attn.h"
+#include "qe_device.cuh"
+#include "qe_internal.h"
+
+namespace qe {
+namespace {
+
+typedef unsigned long long u64;
+
+constexpr int kSampleThreads = 512;
+constexpr int kSampleWarps = kSampleThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxVocab = 1 << 19;
+constexpr int kMaxCluster = 16;
+
+struct SampleArgs {
+  const void* logits;
+  long long stride;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  const float* u;
+  int32_t* token;
+  float* logprob;
+  int B, V, shift, run;  // run: elements of the row per CTA
+  int cluster;
+  int smem_row;  // bytes of the row's run in shared memory
+};
+
+// 2^(i / 128): the table of a table-driven exponential (Tang, "Table-driven
+// implementation of the exponential function in IEEE floating-point
+// arithmetic", ACM TOMS 15, 1989), filled once per CTA.
+constexpr int kExpTable = 128;
+
+struct SampleShared {
+  double exp2_table[kExpTable];
+  u64 xch[2][kMaxCluster];   // all-gather slots, two in turn
+  u64 warp_sum[kSampleWarps];
+  u64 found[2][4];           // crossing bin, sum above it, its own sum
+  unsigned hist[3][kBins];   // 16-bit pieces of the weights' sums
+};
+
+QE_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+QE_DEV void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+QE_DEV void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+QE_DEV void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+QE_DEV uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+QE_DEV void st_peer64(uint32_t a, u64 v) { asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory"); }
+QE_DEV uint32_t ld_peer32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Order-preserving key of a logit: larger logit, larger key; -0 as +0; NaN as -inf.
+QE_DEV uint32_t key_of(float x) {
+  x = x == x ? x + 0.f : -INFINITY;
+  const uint32_t b = __float_as_uint(x);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+template <typename T>
+struct Elems;
+template <>
+struct Elems<float> {
+  static constexpr int N = 4;
+  static QE_DEV void get(const uint4& w, float (&x)[4]) {
+    x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
+  }
+  static QE_DEV float lowest() { return -INFINITY; }
+};
+template <typename T>
+struct Elems {
+  static constexpr int N = 8;
+  static QE_DEV void get(const uint4& w, float (&x)[8]) {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack2<T>(v[i]);
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+  static QE_DEV T lowest() { return (T)(-INFINITY); }
+};
+
+QE_DEV u64 warp_scan(u64 v) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const u64 x = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += x;
+  }
+  return v;
+}
+
+template <typename T>
+struct Row {
+  static constexpr int N = Elems<T>::N;
+  const SampleArgs& a;
+  SampleShared& sh;
+  const uint4* data;   // the run as stored; its first piece holds element `first` at 0
+  int pieces, per_thread;
+  int first;           // index in the row of element 0 of piece 0 (may be below the run's start)
+  uint32_t rank, size;
+  int turn = 0, turn_found = 0;
+  float x_max = 0.f;
+  double inv_t = 1.0, scale = 1.0;
+  uint32_t thr = 0;    // kept: key > thr, or key == thr and index < cut
+  int cut = 0x7fffffff;
+
+  QE_DEV Row(const SampleArgs& a_, SampleShared& s_) : a(a_), sh(s_) {}
+
+  // f(x, index) over this thread's elements, in index order
+  template <typename F>
+  QE_DEV void each(F f) const {
+    const int p0 = threadIdx.x * per_thread, p1 = min(pieces, p0 + per_thread);
+    for (int p = p0; p < p1; ++p) {
+      float x[N];
+      Elems<T>::get(data[p], x);
+#pragma unroll
+      for (int e = 0; e < N; ++e) f(x[e], first + p * N + e);
+    }
+  }
+
+  // Every CTA's v, by rank, in the returned array (valid until the next but one call).
+  QE_DEV const u64* all_gather(u64 v) {
+    u64* slots = sh.xch[turn];
+    turn ^= 1;
+    if (threadIdx.x < size) st_peer64(peer_addr(slots + rank, threadIdx.x), v);
+    cluster_sync();
+    return slots;
+  }
+  QE_DEV u64 block_sum(u64 v) {
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 4);
+    v += __shfl_xor_sync(0xffffffffu, v, 2);
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh.warp_sum[threadIdx.x >> 5] = v;
+    __syncthreads();
+    u64 s = 0;
+#pragma unroll
+    for (int w = 0; w < kSampleWarps; ++w) s += sh.warp_sum[w];
+    return s;
+  }
+
+  // Weight of a logit as a multiple of 2^-S: e^y = 2^(k / 128) e^r with
+  // k = rint(128 y / ln 2) and |r| <= ln 2 / 256, where four terms after 1
+  // leave r^5 / 120 = 1.2e-15.  The product is below 2^52, so adding 2^52
+  // rounds it to a whole number in the low bits.
+  QE_DEV u64 weight(float x) const {
+    if (x == x_max) return (u64)1 << a.shift;
+    const double y = ((double)x - (double)x_max) * inv_t;
+    if (!(y > -45.0)) return 0;  // below 2^-64; NaN too
+    const double kd = rint(y * 184.66496523378731);
+    const double r = fma(-kd, 0.0054152123481245727, y);
+    const int k = (int)kd;
+    double p = fma(r, 1.0 / 24.0, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    p *= sh.exp2_table[k & (kExpTable - 1)];
+    const double two = __longlong_as_double((long long)(1023 + a.shift + (k >> 7)) << 52);
+    return (u64)__double_as_longlong(fma(p, two, 4503599627370496.0)) & 0xfffffffffffffull;
+  }
+  QE_DEV bool kept(float x, int i) const {
+    const uint32_t k = key_of(x);
+    return k > thr || (k == thr && i < cut);
+  }
+
+  QE_DEV int coarse_bin(float x) const {
+    if (!(x < x_max)) return x == x_max ? 0 : kBins - 1;
+    const int b = (int)(__float_as_uint(x_max - x) >> 16) - ((127 - 8) << 7);
+    return min(max(b, 0), kBins - 1);
+  }
+
+  // Zeroes the histogram; a barrier has to follow before the first add.
+  QE_DEV void hist_clear() {
+    for (int i = threadIdx.x; i < 3 * kBins; i += kSampleThreads) (&sh.hist[0][0])[i] = 0;
+  }
+  QE_DEV void hist_add(int bin, u64 w) {
+    const unsigned lo = (unsigned)w & 0xffffu, mid = (unsigned)(w >> 16) & 0xffffu, hi = (unsigned)(w >> 32);
+    if (lo) atomicAdd(&sh.hist[0][bin], lo);
+    if (mid) atomicAdd(&sh.hist[1][bin], mid);
+    if (hi) atomicAdd(&sh.hist[2][bin], hi);
+  }
+  // The bin in which the cluster's sum, bin 0 first, reaches `target` (1 <=
+  // target <= the total); above: the sum before it.  All CTAs get it.
+  QE_DEV int crossing(u64 target, u64* above) {
+    cluster_sync();  // every CTA's histogram is complete
+    const int per = kBins / size;  // size is a power of two
+    constexpr int kMost = kBins / kSampleThreads;
+    u64 v[kMost];
+    u64 sum = 0;
+    const int b0 = rank * per;
+    // thread t: bins [t * m, (t + 1) * m) of this CTA's slice
+    const int m = per >= kSampleThreads ? per / kSampleThreads : 1;
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+      v[j] = 0;
+      const int i = threadIdx.x * m + j;
+      if (j < m && i < per)
+        for (uint32_t r = 0; r < size; ++r) {
+          v[j] += (u64)ld_peer32(peer_addr(&sh.hist[0][b0 + i], r));
+          v[j] += (u64)ld_peer32(peer_addr(&sh.hist[1][b0 + i], r)) << 16;
+          v[j] += (u64)ld_peer32(peer_addr(&sh.hist[2][b0 + i], r)) << 32;
+        }
+      sum += v[j];
+    }
+    u64 scan = warp_scan(sum);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 31) sh.warp_sum[threadIdx.x >> 5] = scan;
+    __syncthreads();
+    u64 total = 0;
+#pragma unroll
+    for (int w = 0; w < kSampleWarps; ++w) {
+      if (w < (int)(threadIdx.x >> 5)) scan += sh.warp_sum[w];
+      total += sh.warp_sum[w];
+    }
+    const u64* slices = all_gather(total);
+    u64 before = scan - sum;
+    for (uint32_t r = 0; r < rank; ++r) before += slices[r];
+    u64* out = sh.found[turn_found];
+    turn_found ^= 1;
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+      if (before < target && target <= before + v[j])
+        for (uint32_t r = 0; r < size; ++r) {
+          st_peer64(peer_addr(out, r), (u64)(b0 + threadIdx.x * m + j));
+          st_peer64(peer_addr(out + 1, r), before);
+        }
+      before += v[j];
+    }
+    cluster_sync();
+    *above = out[1];
+    return (int)out[0];
+  }
+
+  // Smallest index i with sum_{j <= i} w(x_j, j) > target, given that the
+  // row's total exceeds target; all threads of all CTAs get it.
+  template <typename F>
+  QE_DEV int locate(F w, u64 target) {
+    u64 mine = 0;
+    each([&](float x, int i) { mine += w(x, i); });
+    u64 scan = warp_scan(mine);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 31) sh.warp_sum[threadIdx.x >> 5] = scan;
+    __syncthreads();
+    u64 total = 0;
+#pragma unroll
+    for (int k = 0; k < kSampleWarps; ++k) {
+      if (k < (int)(threadIdx.x >> 5)) scan += sh.warp_sum[k];
+      total += sh.warp_sum[k];
+    }
+    const u64* runs = all_gather(total);
+    u64 before = scan - mine;
+    for (uint32_t r = 0; r < rank; ++r) before += runs[r];
+    u64* out = sh.found[turn_found];
+    turn_found ^= 1;
+    if (before <= target && target < before + mine) {
+      int at = -1;
+      each([&](float x, int i) {
+        before += w(x, i);
+        if (at < 0 && before > target) at = i;
+      });
+      for (uint32_t r = 0; r < size; ++r) st_peer64(peer_addr(out, r), (u64)at);
+    }
+    cluster_sync();
+    return (int)out[0];
+  }
+
+  // Cuts the kept elements, in descending order, to the shortest run whose sum
+  // of w reaches target (1 <= target <= their sum).  w is 0 for what is not kept.
+  template <typename F>
+  QE_DEV void cut_at(F w, u64 target) {
+    hist_clear();
+    __syncthreads();
+    each([&](float x, int i) {
+      const u64 v = w(x, i);
+      if (v) hist_add(coarse_bin(x), v);
+    });
+    u64 above;
+    const int bin = crossing(target, &above);
+    target -= above;
+    // keys that the bin can hold: its bounds on x_max - x, widened by two
+    // units in the last place of that difference
+    uint32_t k_hi = key_of(x_max), k_lo = key_of(-INFINITY);
+    const double d_lo = (double)__uint_as_float((uint32_t)(bin + ((127 - 8) << 7)) << 16);
+    const double d_hi = (double)__uint_as_float((uint32_t)(bin + 1 + ((127 - 8) << 7)) << 16);
+    if (bin > 0) k_hi = min(k_hi, key_of(__double2float_ru((double)x_max - d_lo * (1.0 - 2.4e-7))));
+    if (bin < kBins - 1 && x_max < INFINITY) k_lo = key_of(__double2float_rd((double)x_max - d_hi * (1.0 + 2.4e-7)));
+    if (bin < kBins - 1 && x_max == INFINITY) k_lo = k_hi;
+    for (;;) {
+      const uint32_t range = k_hi - k_lo;
+      const int bits = 32 - __clz(range | 1);
+      const int sh_bits = bits > 11 ? bits - 11 : 0;
+      hist_clear();  // crossing() ends well after the last peer's read
+      __syncthreads();
+      each([&](float x, int i) {
+        const uint32_t k = key_of(x);
+        if (k < k_lo || k > k_hi || coarse_bin(x) != bin) return;
+        const u64 v = w(x, i);
+        if (v) hist_add((int)((k_hi - k) >> sh_bits), v);
+      });
+      const int b = crossing(target, &above);
+      target -= above;
+      k_hi -= (uint32_t)b << sh_bits;
+      if (sh_bits == 0) break;
+      const uint32_t width = (1u << sh_bits) - 1;
+      k_lo = k_hi - k_lo > width ? k_hi - width : k_lo;
+    }
+    // of the elements with key k_hi, as many of the lowest indices as it takes
+    auto tie = [&](float x, int i) -> u64 { return key_of(x) == k_hi ? w(x, i) : 0; };
+    u64 mine = 0;
+    each([&](float x, int i) { mine += tie(x, i); });
+    const u64* runs = all_gather(block_sum(mine));
+    u64 all = 0;
+    for (uint32_t r = 0; r < size; ++r) all += runs[r];
+    int at = thr == k_hi ? cut : 0x7fffffff;
+    if (all > target) {
+      const int last = locate(tie, target - 1);  // the run ends with the tie that reaches the target
+      at = min(at, last + 1);
+    }
+    thr = k_hi;
+    cut = at;
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int N = Elems<T>::N;
+  SampleShared& sh = *reinterpret_cast<SampleShared*>(smem + a.smem_row);
+  const int row = blockIdx.x / a.cluster;
+  Row<T> r(a, sh);
+  r.size = a.cluster;
+  r.rank = a.cluster > 1 ? cluster_rank() : 0;
+
+  cluster_arrive();  // waited for before the first access to a peer: it has to be running
+  if (threadIdx.x < kExpTable) sh.exp2_table[threadIdx.x] = exp2((double)threadIdx.x / kExpTable);
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // this CTA's run of the row, element for element as stored, from the
+  // 16-byte boundary at or before it
+  const T* base = (const T*)a.logits + (size_t)row * a.stride;
+  const int i0 = min(a.V, (int)r.rank * a.run), i1 = min(a.V, i0 + a.run);
+  {
+    const T* p0 = base + i0;
+    const int skew = (int)(((uintptr_t)p0 & 15) / sizeof(T));
+    const int n = i1 - i0;
+    r.first = i0 - skew;
+    r.pieces = n > 0 ? (skew + n + N - 1) / N : 0;
+    r.per_thread = ((r.pieces + kSampleThreads - 1) / kSampleThreads) | 1;
+    r.data = reinterpret_cast<const uint4*>(smem);
+    T* dst = reinterpret_cast<T*>(smem);
+    const T* src = p0 - skew;
+    for (int p = threadIdx.x; p < r.pieces; p += kSampleThreads) {
+      if (p * N >= skew && (p + 1) * N <= skew + n) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst + p * N)), "l"(src + p * N) : "memory");
+      } else {
+        for (int e = p * N; e < (p + 1) * N; ++e)
+          dst[e] = e >= skew && e < skew + n ? src[e] : Elems<T>::lowest();
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+  }
+
+  // the largest logit, the lowest index of its ties
+  float best = -INFINITY;
+  int best_i = 0x7fffffff;
+  r.each([&](float x, int i) {
+    if (x > best) {
+      best = x;
+      best_i = i;
+    }
+  });
+  u64 top = ((u64)key_of(best) << 32) | (uint32_t)~best_i;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    const u64 x = __shfl_xor_sync(0xffffffffu, top, d);
+    top = x > top ? x : top;
+  }
+  if ((threadIdx.x & 31) == 0) sh.warp_sum[threadIdx.x >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSampleWarps; ++w) top = sh.warp_sum[w] > top ? sh.warp_sum[w] : top;
+  cluster_wait();
+  const u64* tops = r.all_gather(top);
+  for (uint32_t k = 0; k < r.size; ++k) top = tops[k] > top ? tops[k] : top;
+  const uint32_t k_max = (uint32_t)(top >> 32);
+  r.x_max = __uint_as_float(k_max & 0x80000000u ? k_max ^ 0x80000000u : ~k_max);
+  const bool first = r.rank == 0 && threadIdx.x == 0;
+  if (r.x_max == -INFINITY) {  // nothing to choose from
+    if (first) {
+      a.token[row] = -1;
+      if (a.logprob) a.logprob[row] = -INFINITY;
+    }
+    cluster_sync();
+    return;
+  }
+  const float t = a.temperature ? a.temperature[row] : 1.f;
+  if (!(t > 0.f)) {  // greedy
+    if (first) {
+      a.token[row] = (int)~(uint32_t)top;
+      if (a.logprob) a.logprob[row] = 0.f;
+    }
+    cluster_sync();
+    return;
+  }
+  r.inv_t = 1.0 / (double)t;
+
+  const int k = a.top_k ? a.top_k[row] : 0;
+  if (k > 0 && k < a.V) r.cut_at([&](float, int i) -> u64 { return i >= i0 && i < i1 ? 1 : 0; }, (u64)k);
+  auto mass = [&](float x, int i) -> u64 { return r.kept(x, i) ? r.weight(x) : 0; };
+  const float tp = a.top_p ? a.top_p[row] : 1.f;
+  if (tp < 1.f) {
+    u64 mine = 0;
+    r.each([&](float x, int i) { mine += mass(x, i); });
+    const u64* runs = r.all_gather(r.block_sum(mine));
+    u64 total = 0;
+    for (uint32_t j = 0; j < r.size; ++j) total += runs[j];
+    // the least whole number that is at least top_p total: top_p = f 2^-e
+    // with a 24-bit f, total below 2^63
+    u64 target = 1;
+    if (tp > 0.f) {
+      int e;
+      const u64 f = (u64)(frexpf(tp, &e) * 16777216.f);
+      const int s = 24 - e;  // top_p = f 2^-s, s >= 24
+      const u64 hi = __umul64hi(f, total), lo = f * total;
+      u64 w = 0;
+      bool rest;
+      if (s < 64) {
+        w = (hi << (64 - s)) | (lo >> s);
+        rest = (lo & (((u64)1 << s) - 1)) != 0;
+      } else if (s < 128) {
+        w = s == 64 ? hi : hi >> (s - 64);
+        rest = lo != 0 || (s > 64 && (hi & (((u64)1 << (s - 64)) - 1)) != 0);
+      } else {
+        rest = true;
+      }
+      target = w + (rest ? 1 : 0);
+      if (target < 1) target = 1;
+    }
+    r.cut_at(mass, target);
+  }
+  const float mp = a.min_p ? a.min_p[row] : 0.f;
+  u64 least = 1;
+  if (mp > 0.f) least = (u64)ceil((double)fminf(mp, 1.f) * (double)((u64)1 << a.shift));
+  if (least < 1) least = 1;
+  auto final_mass = [&](float x, int i) -> u64 {
+    const u64 w = mass(x, i);
+    return w >= least ? w : 0;
+  };
+  u64 mine = 0;
+  r.each([&](float x, int i) { mine += final_mass(x, i); });
+  const u64* runs = r.all_gather(r.block_sum(mine));
+  u64 total = 0;
+  for (uint32_t j = 0; j < r.size; ++j) total += runs[j];
+  // floor(u total), exactly: u = f 2^-s
+  const float uu = a.u[row];
+  u64 target = 0;
+  if (uu >= 1.f) {
+    target = total - 1;
+  } else if (uu > 0.f) {
+    int e;
+    const u64 f = (u64)(frexpf(uu, &e) * 16777216.f);
+    const int s = 24 - e;
+    const u64 hi = __umul64hi(f, total), lo = f * total;
+    target = s < 64 ? (hi << (64 - s)) | (lo >> s) : s < 128 ? (s == 64 ? hi : hi >> (s - 64)) : 0;
+  }
+  const int token = r.locate(final_mass, target);
+  if (token >= i0 && token < i1) {
+    const int local = token - r.first;
+    if (threadIdx.x == local / N / r.per_thread) {
+      const float x = (float)reinterpret_cast<const T*>(smem)[local];
+      a.token[row] = token;
+      if (a.logprob) a.logprob[row] = (float)log((double)r.weight(x) / (double)total);
+    }
+  }
+  cluster_sync();
+}
+
+template <typename T>
+cudaError_t launch_sample_t(SampleArgs a, cudaStream_t s) {
+  // CTAs per row: enough that a CTA's run is short (latency) and fits in shared memory
+  const int es = (int)sizeof(T);
+  int cl = 1;
+  while (cl < 8 && (long long)a.V * es / cl > 32768) cl *= 2;
+  if ((long long)a.V * es / cl > 160 * 1024) cl = 16;
+  a.cluster = cl;
+  const int n = 16 / es;
+  a.run = ((a.V + cl - 1) / cl + n - 1) / n * n;
+  a.smem_row = (a.run + 2 * n) * es;
+  a.smem_row = (a.smem_row + 127) / 128 * 128;
+  const int bytes = a.smem_row + (int)sizeof(SampleShared);
+  static std::atomic<bool> set[64];  // per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!set[dev]) {
+    e = cudaFuncSetAttribute(qe_sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(qe_sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.B * cl));
+  cfg.blockDim = dim3(kSampleThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cl;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, qe_sample_kernel<T>, a);
+}
+
+}  // namespace
+}  // namespace qe
+
+using namespace qe;
+
+extern "C" QE_API int token_sample(const void* logits, int dtype, int B, int V, int64_t stride, const float* temperature,
+                                   const int32_t* top_k, const float* top_p, const float* min_p, const float* u,
+                                   int32_t* token, float* logprob, qe_stream_t stream) {
+  if (!(dtype == QE_F32 || dtype == QE_BF16 || dtype == QE_F16))
+    return fail(QE_ERR_INVALID_ARG, "dtype must be QE_F32, QE_BF16 or QE_F16 (got %d)", dtype);
+  if (B < 0 || B > 1 << 20) return fail(QE_ERR_INVALID_ARG, "B must be in [0, 2^20] (got %d)", B);
+  if (V < 1 || V > kMaxVocab) return fail(QE_ERR_INVALID_ARG, "V must be in [1, %d] (got %d)", kMaxVocab, V);
+  if (B > 1 && stride < V) return fail(QE_ERR_INVALID_ARG, "stride must be at least V");
+  if (B == 0) return QE_OK;
+  int rc;
+  if ((rc = check_ptr(logits, "logits", false, dtype == QE_F32 ? 4 : 2)) || (rc = check_ptr(temperature, "temperature", true)) ||
+      (rc = check_ptr(top_k, "top_k", true)) || (rc = check_ptr(top_p, "top_p", true)) || (rc = check_ptr(min_p, "min_p", true)) ||
+      (rc = check_ptr(u, "u")) || (rc = check_ptr(token, "token")) || (rc = check_ptr(logprob, "logprob", true)))
+    return rc;
+  SampleArgs a{};
+  a.logits = logits; a.stride = stride; a.temperature = temperature; a.top_k = top_k; a.top_p = top_p; a.min_p = min_p;
+  a.u = u; a.token = token; a.logprob = logprob; a.B = B; a.V = V;
+  int bits = 0;
+  while ((1 << bits) < V) ++bits;
+  a.shift = 62 - bits < 46 ? 62 - bits : 46;
+  const cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = dtype == QE_F32 ? launch_sample_t<float>(a, s)
+                        : dtype == QE_BF16 ? launch_sample_t<__nv_bfloat16>(a, s) : launch_sample_t<__half>(a, s);
+  if (e != cudaSuccess) return cuda_fail(e, "token_sample launch");
+  return QE_OK;
+}

@@ -1,0 +1,457 @@
+"""attn_kv_append and attn_decode_step on the GPU against their 64-bit
+definitions (_decode_ref), element by element within bounds that count the
+roundings (derived there), and the calls' conventions: padding rows, bad pages,
+strides, graphs, streams."""
+import math
+
+import numpy as np
+import pytest
+
+import _decode_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def q(cuda):
+    import quantized_expert_matvec_b200 as q
+    return q
+
+
+def dt(name):
+    import torch
+    return {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[name]
+
+
+def host(t):
+    return t.double().cpu().numpy()
+
+
+# ------------------------------------------------------------------- append
+
+APPEND = [
+    # src, cache, T, n_q, n_kv, D, rd, axes, adjacent, page, far
+    ("bf16", "bf16", 1, 4, 2, 128, 128, 1, False, 16, 100),
+    ("f32", "bf16", 7, 6, 2, 64, 64, 1, True, 1, 5),
+    ("f32", "f16", 33, 8, 1, 256, 64, 3, False, 24, 1000003),
+    ("f16", "f16", 5, 3, 3, 128, 96, 2, True, 5, 2147480000),
+    ("bf16", "f16", 130, 40, 8, 128, 16, 4, False, 64, 70000),
+    ("f16", "bf16", 9, 1, 1, 64, 0, 1, False, 128, 9),
+    ("f32", "f16", 3, 70, 7, 256, 256, 1, False, 65536, 131072),
+]
+
+
+def append_inputs(c, seed):
+    import torch
+    src, cache, T, n_q, n_kv, D, rd, axes, adjacent, page, far = c
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rng = np.random.RandomState(seed)
+    x = torch.randn((T, (n_q + 2 * n_kv) * D + 8), generator=g, device="cuda").to(dt(src))  # strided tokens
+    n_seq = max(1, T // 3)
+    cols = 2 if page > 1000 else (T + 3 * page) // page + 1
+    places = rng.permutation(n_seq * cols * min(page, 64))[:T]  # distinct
+    seq, kv_pos = places % n_seq, (places // n_seq)
+    n_pages = n_seq * cols + 2
+    d = dict(q=x[:, :n_q * D].unflatten(1, (n_q, D)), k=x[:, n_q * D:(n_q + n_kv) * D].unflatten(1, (n_kv, D)),
+             v=x[:, (n_q + n_kv) * D:(n_q + 2 * n_kv) * D].unflatten(1, (n_kv, D)))
+    if page > 1000:
+        n_seq, n_pages = 1, 3
+        seq, kv_pos = np.zeros(T, np.int64), page - 2 + np.arange(T)
+        d["table"] = torch.tensor([[2, 0]], dtype=torch.int32, device="cuda")
+    else:
+        d["table"] = torch.from_numpy(rng.permutation(n_pages)[:n_seq * cols].reshape(n_seq, cols).astype(np.int32)).cuda()
+    if T > 4:
+        kv_pos[2] = -1
+        kv_pos[T - 1] = -2147483648
+    d["seq"] = torch.from_numpy(seq.astype(np.int32)).cuda()
+    d["kv_pos"] = torch.from_numpy(kv_pos.astype(np.int32)).cuda()
+    d["pos"] = torch.from_numpy(rng.randint(0, far + 1, (axes, T)).astype(np.int32)).cuda()
+    for n in ("kp", "vp"):
+        d[n] = torch.full((n_pages, n_kv, page, D), 3.0, device="cuda").to(dt(cache))
+    d["out"] = torch.full((T, n_q, D), -5.0, device="cuda").to(dt(cache))
+    half = rd // 2
+    d["axis"] = [i % axes for i in range(half)]
+    d["inv_freq"] = (10000.0 ** (-torch.arange(half, dtype=torch.float64) / max(half, 1))).to(torch.float32).cuda()
+    return d
+
+
+def check_append(c, d):
+    src, cache, T, n_q, n_kv, D, rd, axes, adjacent, page, far = c
+    kv_pos, seq, table = (d[n].cpu().numpy() for n in ("kv_pos", "seq", "table"))
+    pos, f = d["pos"].cpu().numpy(), d["inv_freq"].cpu().numpy()
+    want_q, size_q = ref.rotate(host(d["q"]), pos, f, d["axis"], adjacent)
+    want_k, size_k = ref.rotate(host(d["k"]), pos, f, d["axis"], adjacent)
+    want_v = host(d["v"])
+
+    def close(got, want, size):
+        # sine and cosine are off by at most 2^-23 (the reduced angle's rounding and the
+        # polynomial), two products and a sum by U32 each; then half a step of the cache's type
+        e = (2.0 ** -23 + 2 * ref.U32) * size
+        tol = e + ref.HALF_STEP[cache] * (np.abs(want) + e) + ref.TINY[cache]
+        assert np.all(np.abs(got - want) <= tol), np.max(np.abs(got - want) - tol)
+
+    live = kv_pos >= 0
+    out = host(d["out"])
+    close(out[live], want_q[live], size_q[live])
+    assert np.all(out[~live] == -5.0)
+    for got, want, size in ((host(d["kp"]), want_k, size_k), (host(d["vp"]), want_v, np.zeros_like(want_v))):
+        touched = np.zeros((got.shape[0], page), bool)
+        for t in np.nonzero(live)[0]:
+            p = table[seq[t], kv_pos[t] // page]
+            close(got[p, :, kv_pos[t] % page], want[t], size[t])
+            touched[p, kv_pos[t] % page] = True
+        assert np.all(got.transpose(0, 2, 1, 3)[~touched] == 3.0)
+
+
+@pytest.mark.parametrize("c", APPEND, ids=lambda c: "-".join(str(x) for x in c))
+def test_append_matches_the_definition(q, cuda, c):
+    d = append_inputs(c, 3)
+    kc = q.KVCache(d["kp"], d["vp"])
+    ws = q.attn_workspace(kc, c[3], 1)
+    rope = q.Rope(d["inv_freq"], d["axis"], c[8], n_axes=c[7]) if c[6] else q.Rope(d["inv_freq"], n_axes=c[7])
+    q.attn_kv_append(kc, d["q"], d["k"], d["v"], d["table"], d["kv_pos"], d["out"], rope=rope, pos=d["pos"],
+                     seq=d["seq"], ws=ws)
+    assert q.qe_workspace_status(ws) == q.QE_OK
+    check_append(c, d)
+
+
+def test_append_without_rotation_copies_bits(q, cuda):
+    # no rope: q_out and the cache hold the inputs' bits, infinities and NaN too; seq None is the token's number
+    import torch
+    T, n_q, n_kv, D, page = 4, 2, 1, 64, 8
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((T, n_q + 2 * n_kv, D), generator=g, device="cuda").to(torch.float16)
+    x[1, :, 3], x[2, :, 5], x[3, :, 7] = math.inf, -math.inf, NAN
+    kp = torch.zeros((T, n_kv, page, D), dtype=torch.float16, device="cuda")
+    vp = torch.zeros_like(kp)
+    kc = q.KVCache(kp, vp)
+    ws = q.attn_workspace(kc, n_q, 1)
+    out = torch.zeros((T, n_q, D), dtype=torch.float16, device="cuda")
+    table = torch.arange(T, dtype=torch.int32, device="cuda").flip(0).reshape(T, 1).contiguous()
+    kv_pos = torch.tensor([0, 7, 3, 1], dtype=torch.int32, device="cuda")
+    q.attn_kv_append(kc, x[:, :n_q], x[:, n_q:n_q + n_kv], x[:, n_q + n_kv:], table, kv_pos, out, ws=ws)
+    assert torch.equal(out.view(torch.int16), x[:, :n_q].contiguous().view(torch.int16))
+    for t in range(T):
+        for pages, head in ((kp, n_q), (vp, n_q + 1)):
+            assert torch.equal(pages[T - 1 - t, 0, kv_pos[t]].view(torch.int16), x[t, head].view(torch.int16))
+    # q in place, then keys alone (no queries)
+    y = x.clone()
+    rope = q.Rope(torch.rand(32, device="cuda"))
+    pos = torch.tensor([[5, 6, 7, 8]], dtype=torch.int32, device="cuda")
+    q.attn_kv_append(kc, x[:, :n_q], x[:, n_q:n_q + 1], x[:, n_q + 1:], table, kv_pos, out, rope=rope, pos=pos, ws=ws)
+    k_ref = kp.clone()
+    q.attn_kv_append(kc, y[:, :n_q], y[:, n_q:n_q + 1], y[:, n_q + 1:], table, kv_pos, y[:, :n_q], rope=rope, pos=pos, ws=ws)
+    assert torch.equal(y[:, :n_q].contiguous().view(torch.int16), out.view(torch.int16))
+    assert torch.equal(y[:, n_q:].contiguous().view(torch.int16), x[:, n_q:].contiguous().view(torch.int16))
+    q.attn_kv_append(kc, None, x[:, n_q:n_q + 1], x[:, n_q + 1:], table, kv_pos, rope=rope, pos=pos, ws=ws)
+    assert torch.equal(kp.view(torch.int16), k_ref.view(torch.int16))
+    assert q.qe_workspace_status(ws) == q.QE_OK
+
+
+def test_append_records_bad_places_and_writes_nothing_there(q, cuda):
+    import torch
+    T, D, page = 5, 64, 8
+    x = torch.ones((T, 3, D), dtype=torch.bfloat16, device="cuda")
+    kp = torch.zeros((3, 1, page, D), dtype=torch.bfloat16, device="cuda")
+    vp = torch.zeros_like(kp)
+    kc = q.KVCache(kp, vp)
+    ws = q.attn_workspace(kc, 1, 1)
+    out = torch.zeros((T, 1, D), dtype=torch.bfloat16, device="cuda")
+    table = torch.tensor([[0, 3], [-1, 1]], dtype=torch.int32, device="cuda")
+    for seq, at in ((0, 8), (1, 0), (0, 16), (2, 0), (-1, 0)):  # page 3 of 3; page -1; column 2 of 2; sequence 2 of 2
+        s = torch.zeros(T, dtype=torch.int32, device="cuda")
+        p = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+        s[3], p[3] = seq, at
+        s[1], p[1] = 1, 9  # a good one beside it
+        out.zero_()
+        kp.zero_()
+        q.attn_kv_append(kc, x[:, :1], x[:, 1:2], x[:, 2:], table, p, out, seq=s, ws=ws)
+        assert q.qe_workspace_status(ws) == q.QE_ERR_INVALID_ARG
+        assert q.qe_workspace_status(ws) == q.QE_OK
+        assert bool((out[3] == 1).all()) and bool((out[1] == 1).all()) and bool((out[[0, 2, 4]] == 0).all())
+        assert float(kp.float().sum()) == D and bool((kp[1, 0, 1] == 1).all())
+
+
+# ---------------------------------------------------------------- attention
+
+def attend_inputs(dtype, D, n_kv, G, page, prefix, lens, seed=0, cols=None, gap=0, scale_q=1.0):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rng = np.random.RandomState(seed)
+    B = len(lens)
+    n_pre = -(-prefix // page)
+    cols = cols or max(1, max(-(-max(n, 0) // page) for n in lens))
+    n_pages = n_pre + B * cols + 2
+    order = rng.permutation(n_pages).astype(np.int32)
+    d = dict(B=B, dtype=dtype, D=D, n_kv=n_kv, G=G, page=page, prefix=prefix, lens=list(lens))
+    d["pp"], d["tb"] = order[:n_pre], order[n_pre:n_pre + B * cols].reshape(B, cols).copy()
+    for n in ("kp", "vp"):
+        pool = torch.full((n_pages, n_kv * page * D + gap), NAN, device="cuda", dtype=dt(dtype))
+        d[n] = pool[:, :n_kv * page * D].unflatten(1, (n_kv, page, D))
+        full = torch.randn((n_pages, n_kv, page, D), generator=g, device="cuda").to(dt(dtype))
+        # what no row may read stays NaN: the ends of last pages, unused pages
+        for i in range(n_pre):
+            m = min(page, prefix - i * page)
+            d[n][order[i], :, :m] = full[order[i], :, :m]
+        for b in range(B):
+            for j in range(cols):
+                m = min(page, max(lens[b], 0) - j * page)
+                if m > 0:
+                    d[n][d["tb"][b, j], :, :m] = full[d["tb"][b, j], :, :m]
+    d["q"] = (scale_q * torch.randn((B, n_kv * G, D), generator=g, device="cuda")).to(dt(dtype))
+    d["scale"] = 1.3 / math.sqrt(D)
+    return d
+
+
+def run_attend(q, d, ws=None, out=None, stream=None):
+    import torch
+    kc = q.KVCache(d["kp"], d["vp"])
+    n_q = d["n_kv"] * d["G"]
+    ws = ws if ws is not None else q.attn_workspace(kc, n_q, d["B"])
+    out = out if out is not None else torch.full((d["B"], n_q, d["D"]), 7.0, device="cuda").to(dt(d["dtype"]))
+    lse = torch.full((d["B"], n_q), 7.0, device="cuda")
+    q.attn_decode_step(kc, d["q"], out, torch.from_numpy(d["tb"]).cuda(),
+                       torch.tensor(d["lens"], dtype=torch.int32, device="cuda"),
+                       torch.from_numpy(d["pp"]).cuda() if d["prefix"] else None, d["prefix"], d["scale"], lse, ws, stream)
+    return out, lse, ws
+
+
+def check_attend(d, out, lse, rows=None, skip_keys=()):
+    kp, vp, qq = host(d["kp"]), host(d["vp"]), host(d["q"])
+    out, lse = host(out), lse.double().cpu().numpy()
+    G = d["G"]
+    for b in rows if rows is not None else range(d["B"]):
+        if d["lens"][b] < 0:
+            assert np.all(out[b] == 7.0) and np.all(lse[b] == 7.0)
+            continue
+        for h in range(d["n_kv"]):
+            k, v = (np.concatenate([ref.gather(p, d["page"], d["pp"], d["prefix"], h),
+                                    ref.gather(p, d["page"], d["tb"][b], d["lens"][b], h)]) for p in (kp, vp))
+            keep = [j for j in range(len(k)) if (b, j) not in skip_keys]
+            sl = slice(h * G, (h + 1) * G)
+            want, want_lse, tol, tol_lse = ref.attend(qq[b, sl], k[keep], v[keep], d["scale"], d["dtype"])
+            bad = np.abs(out[b, sl] - want) - tol
+            assert np.all(bad <= 0), (b, h, bad.max())
+            with np.errstate(invalid="ignore"):
+                ok = (lse[b, sl] == want_lse) | (np.abs(lse[b, sl] - want_lse) <= tol_lse)
+            assert ok.all(), (b, h, lse[b, sl], want_lse)
+
+
+ATTEND = [
+    # dtype, D, n_kv, G, page, prefix, lens
+    ("bf16", 128, 2, 4, 16, 0, [1]),
+    ("f16", 128, 1, 1, 16, 0, [0, 1, 15, 16, 17, 63, 64, 65]),
+    ("bf16", 64, 2, 5, 1, 0, [33, 0, 129]),
+    ("f16", 256, 1, 16, 24, 70, [0, 1, 200]),
+    ("bf16", 128, 3, 7, 5, 1, [0, 0, 3]),
+    ("f16", 64, 1, 17, 64, 64, [10, 300]),
+    ("bf16", 128, 2, 40, 32, 65, [5, -1, 64]),
+    ("bf16", 256, 2, 2, 128, 127, [1] * 9),
+    ("f16", 128, 4, 8, 16, 300, [7, 0, -1, 90, 1000, 2, 31, 32, 33, 4, 5]),
+    ("bf16", 64, 1, 3, 48, 513, [11 * i for i in range(50)]),
+    ("f16", 128, 1, 1, 16, 130, [3] * 70),
+    ("bf16", 128, 8, 4, 16, 1000, [i % 5 for i in range(33)]),
+    ("f16", 64, 2, 4, 8, 2049, [17] * 40),
+    ("bf16", 256, 1, 8, 64, 700, [9, 0, 100] * 11),
+    ("bf16", 128, 1, 1, 16, 0, [3000]),
+]
+
+
+@pytest.mark.parametrize("c", ATTEND, ids=lambda c: f"{c[0]}_d{c[1]}_kv{c[2]}_g{c[3]}_page{c[4]}_pre{c[5]}_b{len(c[6])}")
+def test_attention_matches_the_definition(q, cuda, c):
+    d = attend_inputs(*c, seed=1)
+    out, lse, ws = run_attend(q, d)
+    assert q.qe_workspace_status(ws) == q.QE_OK
+    check_attend(d, out, lse)
+    again, lse2, _ = run_attend(q, d, ws=ws)  # the same workspace, the same bits
+    import torch
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def test_peaked_scores_and_page_gaps(q, cuda):
+    # scores of hundreds (one key takes all), pages apart in a larger pool
+    for prefix, lens in ((0, [200, 9]), (150, [40] * 20)):
+        d = attend_inputs("bf16", 128, 2, 4, 16, prefix, lens, seed=2, gap=4096, scale_q=60.0)
+        out, lse, _ = run_attend(q, d)
+        check_attend(d, out, lse)
+
+
+def test_strided_queries_and_outputs(q, cuda):
+    import torch
+    d = attend_inputs("f16", 64, 2, 2, 16, 20, [30, 5, 70], seed=3)
+    dense, lse, _ = run_attend(q, d)
+    wide = torch.zeros((3, 8, 64), dtype=torch.float16, device="cuda")
+    wide[:, 2:6] = d["q"]
+    d2 = dict(d, q=wide[:, 2:6])
+    into = torch.zeros((3, 12, 64), dtype=torch.float16, device="cuda")
+    out, _, _ = run_attend(q, d2, out=into[:, 4:8])
+    assert torch.equal(out, dense)
+    assert bool((into[:, :4] == 0).all()) and bool((into[:, 8:] == 0).all())
+
+
+def test_bad_pages_are_masked_and_recorded(q, cuda):
+    d = attend_inputs("bf16", 64, 1, 4, 8, 24, [20, 40], seed=4)
+    good = d["tb"][1, 2]
+    d["tb"][1, 2] = len(d["kp"])       # keys 16 .. 23 of row 1
+    out, lse, ws = run_attend(q, d)
+    assert q.qe_workspace_status(ws) == q.QE_ERR_INVALID_ARG
+    d["tb"][1, 2] = good
+    check_attend(d, out, lse, skip_keys={(1, 24 + j) for j in range(16, 24)})
+    d["pp"][1] = -1                    # keys 8 .. 15 of the prefix, for both rows
+    keep = d["pp"].copy()
+    out, lse, _ = run_attend(q, d, ws=ws)
+    assert q.qe_workspace_status(ws) == q.QE_ERR_INVALID_ARG
+    d["pp"][1] = d["pp"][0]
+    check_attend(d, out, lse, skip_keys={(b, j) for b in range(2) for j in range(8, 16)})
+    d["pp"] = keep
+
+
+def test_length_beyond_the_table_is_cut(q, cuda):
+    d = attend_inputs("f16", 64, 1, 2, 8, 0, [16, 16], seed=5)
+    d["lens"] = [16, 17]
+    out, lse, ws = run_attend(q, d)
+    assert q.qe_workspace_status(ws) == q.QE_ERR_INVALID_ARG
+    d["lens"] = [16, 16]
+    check_attend(d, out, lse)
+
+
+def test_no_table_at_all(q, cuda):
+    # table with no columns: every row has the prefix alone
+    import torch
+    d = attend_inputs("bf16", 128, 1, 4, 16, 100, [0, 0, 0], seed=6)
+    full, lse, _ = run_attend(q, d)
+    d["tb"] = np.zeros((3, 0), np.int32)
+    out, lse2, ws = run_attend(q, d)
+    assert q.qe_workspace_status(ws) == q.QE_OK
+    assert torch.equal(out, full) and torch.equal(lse, lse2)
+    check_attend(d, out, lse)
+
+
+def test_a_nan_row_stays_alone(q, cuda):
+    # NaN in one query: that row's heads are NaN, the others untouched by it
+    import torch
+    d = attend_inputs("bf16", 64, 2, 4, 16, 200, [5, 6, 7, 8, 9, 10], seed=7)
+    clean, _, _ = run_attend(q, d)
+    d["q"][2, 1, 0] = NAN
+    out, lse, _ = run_attend(q, d)
+    assert bool(out[2, 1].isnan().all()) and bool(lse[2, 1].isnan())
+    keep = torch.ones((6, 8), dtype=torch.bool, device="cuda")
+    keep[2, 1] = False
+    assert torch.equal(out[keep], clean[keep])
+
+
+def test_offsets_beyond_32_bits(q, cuda):
+    # pages 2^31 elements apart: byte offsets pass 2^32, element offsets 2^31
+    import torch
+    stride = (1 << 30) + 4096
+    pool = torch.empty(3 * stride, dtype=torch.bfloat16, device="cuda")
+    d = attend_inputs("bf16", 64, 1, 2, 16, 16, [13], seed=8)
+    small, lse, _ = run_attend(q, d)
+    far = {}
+    for n, base in (("kp", 0), ("vp", 8192)):
+        far[n] = torch.as_strided(pool, (3, 1, 16, 64), (stride, 1024, 64, 1), base)
+        far[n][2] = d[n][d["pp"][0]]
+        far[n][1] = d[n][d["tb"][0, 0]]
+    d2 = dict(d, kp=far["kp"], vp=far["vp"], pp=np.array([2], np.int32), tb=np.array([[1]], np.int32))
+    out, lse2, ws = run_attend(q, d2)
+    assert torch.equal(out, small) and torch.equal(lse, lse2)
+    # and the append reaches them
+    kc = q.KVCache(far["kp"], far["vp"])
+    x = torch.ones((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    one = torch.tensor([[2]], dtype=torch.int32, device="cuda")
+    q.attn_kv_append(kc, None, x, 2 * x, one, torch.tensor([15], dtype=torch.int32, device="cuda"), ws=ws)
+    assert bool((far["kp"][2, 0, 15] == 1).all()) and bool((far["vp"][2, 0, 15] == 2).all())
+    del pool, far
+
+
+def test_rows_of_one_sequence_give_a_causal_block(q, cuda):
+    # several query tokens of one sequence: rows with the same pages, lengths one apart
+    d = attend_inputs("f16", 128, 2, 2, 16, 40, [10, 11, 12, 13], seed=9)
+    d["tb"][:] = d["tb"][3]
+    out, lse, _ = run_attend(q, d)
+    check_attend(d, out, lse)
+
+
+def test_graphs_sharing_a_workspace_follow_new_lengths(q, cuda):
+    # two captured calls on one workspace, replayed in turn; lengths change between replays
+    import torch
+    ds = [attend_inputs("bf16", 128, 2, 4, 16, 100, [50, 3, 90, 0], seed=10, cols=8),
+          attend_inputs("f16", 64, 4, 2, 8, 0, [20, 64], seed=11, cols=8)]
+    calls, ws = [], None
+    for d in ds:
+        kc = q.KVCache(d["kp"], d["vp"])
+        n = q.attn_workspace_bytes(kc, d["n_kv"] * d["G"], d["B"])
+        if ws is None or ws.numel() < n:
+            ws = q.attn_workspace(kc, d["n_kv"] * d["G"], d["B"])
+    s = torch.cuda.Stream()
+    for d in ds:
+        kc = q.KVCache(d["kp"], d["vp"])
+        n_q = d["n_kv"] * d["G"]
+        out = torch.full((d["B"], n_q, d["D"]), 7.0, device="cuda").to(dt(d["dtype"]))
+        lse = torch.full((d["B"], n_q), 7.0, device="cuda")
+        tb, pp = torch.from_numpy(d["tb"]).cuda(), torch.from_numpy(d["pp"]).cuda()
+        ln = torch.tensor(d["lens"], dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            q.attn_decode_step(kc, d["q"], out, tb, ln, pp if d["prefix"] else None, d["prefix"], d["scale"], lse, ws)
+        calls.append((g, out, lse, ln, tb, pp))  # a graph reads what it captured: all of it stays alive
+    for trim in (0, 1, 2):
+        for d, (g, out, lse, ln, *_) in zip(ds, calls):
+            ln.copy_(torch.tensor([max(n - trim, 0) for n in d["lens"]], dtype=torch.int32))
+        for _ in range(2):
+            for g, *_ in calls:
+                g.replay()
+        torch.cuda.synchronize()
+        for d, (g, out, lse, ln, *_) in zip(ds, calls):
+            e = dict(d, lens=[max(n - trim, 0) for n in d["lens"]])
+            check_attend(e, out, lse)
+    assert q.qe_workspace_status(ws) == q.QE_OK
+
+
+def test_another_stream(q, cuda):
+    import torch
+    d = attend_inputs("bf16", 128, 2, 4, 16, 300, [50, 3, 900], seed=12)
+    want, lse, _ = run_attend(q, d)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        out, lse2, _ = run_attend(q, d)
+    s.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, lse2)
+
+
+def test_empty_batch(q, cuda):
+    import torch
+    d = attend_inputs("bf16", 64, 1, 2, 16, 0, [3], seed=13)
+    kc = q.KVCache(d["kp"], d["vp"])
+    ws = q.attn_workspace(kc, 2, 0)
+    e = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    q.attn_decode_step(kc, e, e.clone(), torch.empty((0, 1), dtype=torch.int32, device="cuda"),
+                       torch.empty(0, dtype=torch.int32, device="cuda"), ws=ws)
+    torch.cuda.synchronize()
+
+
+def test_binding_refuses_before_any_launch(q, cuda):
+    import torch
+    d = attend_inputs("bf16", 64, 1, 2, 16, 16, [3], seed=14)
+    kc = q.KVCache(d["kp"], d["vp"])
+    ws = q.attn_workspace(kc, 2, 1)
+    tb, ln = torch.from_numpy(d["tb"]).cuda(), torch.tensor([3], dtype=torch.int32, device="cuda")
+    out = torch.empty_like(d["q"])
+    with pytest.raises(ValueError, match="out must be"):
+        q.attn_decode_step(kc, d["q"], out.float(), tb, ln, ws=ws)
+    with pytest.raises(ValueError, match="kv_len"):
+        q.attn_decode_step(kc, d["q"], out, tb, ln.long(), ws=ws)
+    with pytest.raises(ValueError, match="prefix_pages"):
+        q.attn_decode_step(kc, d["q"], out, tb, ln, prefix_len=16, ws=ws)
+    with pytest.raises(ValueError, match="heads"):
+        q.attn_decode_step(kc, d["q"].transpose(1, 2).contiguous().transpose(1, 2), out, tb, ln, ws=ws)
+    with pytest.raises(q.QEError, match="too small"):
+        q.attn_decode_step(kc, d["q"], out, tb, ln, ws=ws[:512])
+    with pytest.raises(q.QEError, match="overlaps"):
+        q.attn_decode_step(kc, d["q"], d["q"], tb, ln, ws=ws)
+    with pytest.raises(ValueError, match="pages of k"):
+        q.KVCache(d["kp"].transpose(2, 3), d["vp"].transpose(2, 3))
