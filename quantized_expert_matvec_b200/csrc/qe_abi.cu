@@ -27,6 +27,8 @@ int cuda_fail(cudaError_t e, const char* what) {
   return fail(QE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+unsigned long long wait_budget_ns() { return g_budget_ns; }
+
 static size_t al(size_t v) { return (v + 255) & ~(size_t)255; }
 
 qe_expert pool_descriptor(const qe_cfg* c, void* base, int bits) {

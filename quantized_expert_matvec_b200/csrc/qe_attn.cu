@@ -3,22 +3,39 @@
 //
 //   out[b,i] = sum_j p_j v_j,   p = softmax_j(scale q[b,i] . k_j)
 //
-// over the prefix's keys, then row b's own.  The keys are cut into chunks; a
-// CTA takes one chunk for 16 query rows of one key head and leaves, per row,
-// the running maximum m and sum l of the softmax and the unnormalised output:
-//   m' = max(m, s),  l' = l 2^(m - m') + 2^(s - m'),  o' = o 2^(m - m') + 2^(s - m') v
-// (scores in log2 units).  A second kernel joins the chunks of a row in a fixed
-// order.  Rows of the prefix are all rows of the batch, so its keys are read
-// once for 16 rows and not once for each.
+// over the prefix's keys, then row b's own.  The work is cut into tiles of 128
+// keys of one key head for a block of query rows: the group's heads of one batch
+// row (own keys), or up to 128 rows of the whole batch (prefix keys, which are
+// therefore read once for all of them).  A persistent CTA per SM takes an equal
+// share of the tiles, whatever the lengths; a run of tiles of one block within a
+// CTA is a segment.  A segment leaves, per query row, a reference m, the sum l of
+// 2^(s - m) (scores s in log2 units) and the output sum o of 2^(s - m) v;
+// the second kernel joins a row's segments in a fixed order:
+//   out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,   M = max m_i.
 //
-// Within a CTA four warps take 16-key tiles in turn, each with its own ring of
-// tiles in shared memory (cp.async), its own m, l and o: no barrier until the
-// four are joined at the end of the chunk.
+// Both products run on the tensor cores with the keys along M, so that a decode
+// step's few rows are a small N and not a padded M:
+//   S^T [128 keys x N]   = K [128 x D] Q^T     (K and Q as they lie: K-major)
+//   O^T [D x N]         += V^T [D x 128] P^T   (V and P as they lie: MN-major)
+// N is the number of rows rounded up to 16.  Accumulators are in tensor memory: two
+// of S^T, two of O^T.  Roles of the 16 warps:
+//   0-7   softmax: a thread has one key (lane of S^T) and the columns of every other 16;
+//   8-11  producers: K and V rows by cp.async from their pages into a ring of
+//         128-byte-swizzled tiles; keys that do not exist become zeros;
+//   12    one thread issues the products;
+//   13    one thread deals out the CTA's segments, through a ring of descriptors
+//         (each role working them out for itself made the code 160 KB and every
+//         role wait for its instructions).
+// The reference m need not be the maximum: it is raised (and o, l rescaled) only
+// when a score passes it by more than 2^8, which one vote per tile finds.
+// l is the sum of the fp32 numerators; their rounding to the cache's dtype is
+// the one that the second product's operand type asks for.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "qe_attn.h"
 #include "qe_device.cuh"
@@ -27,11 +44,30 @@
 namespace qe {
 namespace {
 
-constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kTileKeys = 16;
-constexpr int kMaxRows = 4096;  // B
+constexpr int kMaxBatch = 4096;  // B
+constexpr int kTile = 128;       // keys per tile
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNoRef = 3.0e38f;  // -m before the first score
+constexpr float kSlack = 8.f;      // a score may pass the reference by this (log2)
+
+constexpr int kSoftWarps = 8, kProdWarps = 4;
+constexpr int kAttnThreads = 512;  // 8 softmax, 4 producer, 1 product warp; 3 fill up the register split
+// registers a thread: 256 x 176 + 256 x 80 = 65536 = 512 x 128, the launch's
+constexpr int kSoftRegs = 176, kOtherRegs = 80;
+
+template <int D>
+struct Shape {
+  static constexpr int kRows = D == 256 ? 64 : 128;        // query rows per block (most N)
+  static constexpr int kParts = D == 256 ? 2 : 1;          // a K or V tile is this many stages
+  static constexpr int kDims = D / kParts;                 // dims per stage
+  static constexpr int kStage = kTile * kDims * 2;         // bytes
+  static constexpr int kQ = kRows * D * 2;
+  static constexpr int kPRow = 128;                        // bytes of a key's line of 64 rows of P
+  static constexpr int kP = 2 * kTile * 128;               // two blocks of 64 rows, or two buffers of one
+  static constexpr int kStages = D == 64 ? 10 : 5;
+  static constexpr int kSmem = 1024 + kStages * kStage + kQ + kP;
+  static_assert(kSmem + 2048 <= 232448, "shared memory of a CTA");
+};
 
 struct AttnArgs {
   const void* q;
@@ -44,427 +80,905 @@ struct AttnArgs {
   const int32_t* kv_len;
   float* lse;
   int* err;
-  float* part_prefix;   // [nsp][B * n_q][D]
-  float2* ml_prefix;    // [nsp][B * n_q] {m, l}
-  float* part_own;      // [chunk][n_q][D]
-  float2* ml_own;
-  int2* own_info;       // [B] {first chunk, chunks}
+  long long* own_start;  // [grid + 1] first own tile of each CTA
+  int2* own_ctas;        // [own block] first and last CTA that work on it
+  int2* prefix_groups;   // [key head] first and last group
+  float2* ml_prefix;     // [slot][B * G] {m, l}
+  float2* ml_own;        // [slot][rows of a block]
+  float* part_prefix;    // [slot][B * G][D]
+  float* part_own;       // [slot][rows of a block][D]
+  unsigned long long budget_ns;
   int B, n_q, n_kv, G, n_pages, table_stride, prefix_len;
-  int nsp, prefix_chunk;  // prefix splits and keys of each
-  int rb_own, rb_prefix;  // blocks of 16 rows per key head
-  int own_target;         // own chunks x key heads x row blocks aimed at
+  int prefix_tiles;      // per key head
+  int groups;            // groups of CTAs, one CTA per row block, that share the prefix
+  int rb_prefix, rb_own; // row blocks per key head
+  int own_rows;          // rows of an own block: min(G, kRows)
   float scale_log2;
   FastDiv page;
 };
 
+// ------------------------------------------------------------ tensor cores
+
+// Shared-memory matrix descriptor, 128-byte swizzle, version 1, in two words: low =
+// address and leading byte offset, high = stride byte offset and the constants.
+// K-major: 1024 (the stride) bytes between groups of 8 rows, the leading offset is not used.
+// MN-major: the leading offset is from one block of 64 elements along M or N to the
+// next, the stride from one group of 8 along K to the next.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+QE_DEV uint32_t desc_low(uint32_t addr, uint32_t lbo) { return ((addr & 0x3ffffu) >> 4) | ((lbo >> 4) << 16); }
+// Instruction descriptor, kind::f16: fp32 accumulator, both operands of T, M = 128.
 template <typename T>
-QE_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
-template <>
-QE_DEV void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+QE_DEV uint32_t mma_idesc(int N, bool mn_major) {
+  const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (type << 7) | (type << 10) | (mn_major ? (1u << 15) | (1u << 16) : 0u) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-template <>
-QE_DEV void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+QE_DEV void mma_issue(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
 }
-QE_DEV void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+QE_DEV void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-QE_DEV void ldmatrix4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+QE_DEV void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+QE_DEV void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+QE_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 16 columns of the warp's 32 lanes
+QE_DEV void tmem_ld16(uint32_t a, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+QE_DEV void tmem_st16(uint32_t a, const float (&v)[16]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Waits for the loads before it; the values are handed through, so that no use moves above it.
+QE_DEV void tmem_wait_ld(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(v[i]));
+}
+QE_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+QE_DEV float exp2_approx(float x) {  // 2^-22 relative; below 2^-126: 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 16 bytes, or 16 zeros
 QE_DEV void cp_async16z(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
 
-template <int D>
-constexpr int kAttnStages = D == 64 ? 6 : 3;
-template <int D>
-constexpr int kAttnTileBytes = kTileKeys * D * 2;  // K or V
-template <int D>
-constexpr int kAttnSmem = kAttnWarps * kAttnStages<D> * 2 * kAttnTileBytes<D>;
+// ------------------------------------------------------------------ shares
 
-// One chunk [k0, k1) of the keys on pages list[0 ..] of key head h, for 16 rows
-// of which `row_src(i)` gives row i's query (NULL: no such row); the result goes
-// to po + row * D and pml[row] with row = row_dst(i).
-template <typename T, int D, typename Src, typename Dst>
-QE_DEV void attn_chunk(const AttnArgs& a, int h, const int32_t* list, int k0, int k1, Src row_src, Dst row_dst,
-                       float* po, float2* pml, unsigned char* smem) {
-  constexpr int S = kAttnStages<D>, TB = kAttnTileBytes<D>;
-  constexpr int CH = D / 8;        // 16-byte pieces of a row
-  constexpr int RPI = 32 / CH;     // rows one warp instruction copies (D = 256: one row)
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned char* ring = smem + warp * S * 2 * TB;
-  const uint32_t ring_u = smem_u32(ring);
-
-  // fragments of the 16 query rows
-  uint32_t qf[D / 16][4];
-  {
-    const T* r0 = (const T*)row_src(lane >> 2);
-    const T* r1 = (const T*)row_src((lane >> 2) + 8);
-    const int c = (lane & 3) * 2;
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      qf[k][0] = r0 ? *reinterpret_cast<const uint32_t*>(r0 + 16 * k + c) : 0u;
-      qf[k][1] = r1 ? *reinterpret_cast<const uint32_t*>(r1 + 16 * k + c) : 0u;
-      qf[k][2] = r0 ? *reinterpret_cast<const uint32_t*>(r0 + 16 * k + c + 8) : 0u;
-      qf[k][3] = r1 ? *reinterpret_cast<const uint32_t*>(r1 + 16 * k + c + 8) : 0u;
-    }
+// How the tiles are dealt out.  Prefix: `groups` groups of one CTA per row block,
+// so that a group reads the same keys at the same time; group g has the tiles
+// [g S / groups, (g + 1) S / groups) of the line (key head, tile) of length S.  More
+// row blocks than CTAs: one group, each CTA takes every grid-th block.  Own: a line
+// (batch row, key head, row block, tile) of which each CTA takes what brings its
+// total to an equal share.
+struct Deal {
+  int grid, R, groups, grouped;
+  long long S, own;
+  QE_DEV Deal(const AttnArgs& a, long long own_tiles) : grid(gridDim.x), R(a.rb_prefix), groups(a.groups), own(own_tiles) {
+    S = (long long)a.prefix_tiles * a.n_kv;
+    grouped = S == 0 ? 0 : R <= grid ? groups * R : grid;
   }
-
-  const int tiles = (k1 - k0 + kTileKeys - 1) / kTileKeys;
-  const int mine = tiles > warp ? (tiles - warp + kAttnWarps - 1) / kAttnWarps : 0;
-  auto first_key = [&](int i) { return k0 + (warp + i * kAttnWarps) * kTileKeys; };
-  // lanes 0..15: the page of key `lane` of my tile i, -1 if there is none
-  auto page_of = [&](int i) {
-    const int key = first_key(i) + (lane & 15);
-    return (i < mine && key < k1) ? __ldg(list + a.page.div((uint32_t)key)) : -1;
-  };
-  int page_next = page_of(0);
-  uint32_t ok_mask[S];  // which keys of the tile in slot s exist
-#pragma unroll
-  for (int s = 0; s < S; ++s) ok_mask[s] = 0;
-  auto issue = [&](int i, int slot) -> uint32_t {
-    uint32_t live = 0;
-    if (i < mine) {
-      const int key = first_key(i) + (lane & 15);
-      const int page = page_next;
-      const bool ok = page >= 0 && page < a.n_pages;
-      if (key < k1 && !ok) set_error(a.err, QE_ERR_INVALID_ARG);
-      live = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-      const int off = key - (int)a.page.div((uint32_t)key) * (int)a.page.d;
-      const long long in_page = ((long long)h * a.page.d + off) * D;
-      const long long ko = ok ? page * a.k_page_stride + in_page : 0, vo = ok ? page * a.v_page_stride + in_page : 0;
-      const uint32_t kd = ring_u + slot * 2 * TB, vd = kd + TB;
-#pragma unroll
-      for (int r = 0; r < kTileKeys / RPI; ++r) {
-        const int row = r * RPI + lane / CH, c = lane % CH;
-        const long long k_at = __shfl_sync(0xffffffffu, ko, row), v_at = __shfl_sync(0xffffffffu, vo, row);
-        const bool real = (live >> row) & 1;
-        const uint32_t at = row * (D * 2) + ((c ^ (row & 7)) << 4);
-        cp_async16z(kd + at, (const T*)a.kc + k_at + c * 8, real);
-        cp_async16z(vd + at, (const T*)a.vc + v_at + c * 8, real);
+  QE_DEV long long group_start(int g) const { return S * g / groups; }
+  QE_DEV long long own_start(int c) const {
+    if (c >= grid) return own;
+    if (S == 0) return own * c / grid;
+    const long long total = own + S * R, each = (S + groups - 1) / groups;
+    if (R <= grid && total / grid >= each) {  // every CTA has room for own tiles
+      long long prefix = S * R;  // prefix tiles of the CTAs before c
+      if (c < grouped) {
+        const int g = c / R;
+        prefix = group_start(g) * R + (group_start(g + 1) - group_start(g)) * (c - g * R);
       }
-      page_next = page_of(i + 1);
+      return total * c / grid - prefix;
     }
-    cp_async_commit();
-    return live;
-  };
-#pragma unroll
-  for (int s = 0; s < S - 1; ++s) ok_mask[s] = issue(s, s);
+    if (grouped < grid) return c <= grouped ? 0 : own * (c - grouped) / (grid - grouped);
+    return own * c / grid;
+  }
+};
 
-  float o[D / 8][4];
-#pragma unroll
-  for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+// A run of tiles of one block: tiles 0 .. n - 1 are keys key0 + 128 i up to kend.
+struct Segment {
+  const int32_t* list;  // pages
+  int key0, kend, n;    // n = 0: no more segments
+  int h, rows;          // key head, query rows
+  int b, row0;          // own: batch row, first head of the group; prefix: -1, first row of B * G
+  int slot;
+};
 
-  for (int i0 = 0; i0 < mine; i0 += S) {
-#pragma unroll
-    for (int u = 0; u < S; ++u) {
-      const int i = i0 + u;
-      if (i >= mine) break;  // uniform over the warp
-      __syncwarp();          // every lane is done with the tile whose slot is refilled now
-      ok_mask[(u + S - 1) % S] = issue(i + S - 1, (u + S - 1) % S);
-      cp_async_wait<S - 1>();
-      __syncwarp();
-      const uint32_t kb = ring_u + u * 2 * TB, vb = kb + TB;
-      const uint32_t live = ok_mask[u];
-      // scores of 16 rows x 16 keys
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        // matrices: keys 0-7 / 8-15 x dims 16k..+7 / +8..+15
-        const int row = (lane & 7) + ((lane >> 4) << 3), c = 2 * k + ((lane >> 3) & 1);
-        uint32_t b[4];
-        ldmatrix4(b, kb + row * (D * 2) + ((c ^ (row & 7)) << 4));
-        mma16816<T>(s0, qf[k], b[0], b[1]);
-        mma16816<T>(s1, qf[k], b[2], b[3]);
-      }
-      // mask, then the running maximum
-      const int c0 = (lane & 3) * 2;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s0[e] = (live >> (c0 + (e & 1))) & 1 ? s0[e] * a.scale_log2 : -INFINITY;
-        s1[e] = (live >> (c0 + 8 + (e & 1))) & 1 ? s1[e] * a.scale_log2 : -INFINITY;
-      }
-      float n0 = fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s1[0], s1[1]));
-      float n1 = fmaxf(fmaxf(s0[2], s0[3]), fmaxf(s1[2], s1[3]));
-      n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, 1));
-      n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, 1));
-      n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, 2));
-      n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, 2));
-      n0 = fmaxf(n0, m0);
-      n1 = fmaxf(n1, m1);
-      const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
-      if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
-        const float f0 = exp2f(m0 - b0), f1 = exp2f(m1 - b1);
-        l0 *= f0;
-        l1 *= f1;
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          o[n][0] *= f0; o[n][1] *= f0;
-          o[n][2] *= f1; o[n][3] *= f1;
-        }
-        m0 = n0;
-        m1 = n1;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s0[e] = exp2f(s0[e] - (e < 2 ? b0 : b1));
-        s1[e] = exp2f(s1[e] - (e < 2 ? b0 : b1));
-      }
-      l0 += (s0[0] + s0[1]) + (s1[0] + s1[1]);
-      l1 += (s0[2] + s0[3]) + (s1[2] + s1[3]);
-      const uint32_t p[4] = {pack2<T>(s0[0], s0[1]), pack2<T>(s0[2], s0[3]), pack2<T>(s1[0], s1[1]), pack2<T>(s1[2], s1[3])};
-#pragma unroll
-      for (int n = 0; n < D / 16; ++n) {
-        // matrices (transposed): keys 0-7 / 8-15 x dims 16n..+7 / +8..+15
-        const int row = lane & 15, c = 2 * n + (lane >> 4);
-        uint32_t b[4];
-        ldmatrix4t(b, vb + row * (D * 2) + ((c ^ (row & 7)) << 4));
-        mma16816<T>(o[2 * n], p, b[0], b[1]);
-        mma16816<T>(o[2 * n + 1], p, b[2], b[3]);
-      }
+constexpr int kSegRing = 8;
+constexpr int kSegReaders = kSoftWarps + kProdWarps + 1;
+
+struct Shared {
+  uint64_t full[10], empty[10];
+  uint64_t s_full[2], p_full[2], p_free[2], q_done[2], o_free[2], seg_full[kSegRing], seg_empty[kSegRing], drained;
+  Segment seg[kSegRing];
+  uint32_t tmem;
+  int abort;
+  uint32_t live[8][kProdWarps];  // which keys of the tile exist, by tile number
+  float neg_ref[128], factor[128];
+  long long sum[16];
+  int found;
+  long long found_start;
+};
+
+// Bounded wait.  Once one has given up, the error is recorded, `abort` is set and
+// every later wait returns at once: the roles walk to their ends (within the same
+// bounds of memory) and the CTA leaves in the ordinary way.
+QE_DEV void wait_for(uint64_t* bar, uint32_t parity, Shared& sh, const AttnArgs& a) {
+  // the timer is read only once the first two tries (the second suspends the
+  // thread for up to 10 us) have failed
+  if (mbar_try_wait(bar, parity) || mbar_try_wait_sleep(bar, parity, 10000u)) return;
+  const uint64_t deadline = gtimer() + a.budget_ns;
+  while (!mbar_try_wait_sleep(bar, parity, 10000u)) {
+    if (*(volatile int*)&sh.abort) return;
+    if (gtimer() > deadline) {
+      *(volatile int*)&sh.abort = 1;
+      set_error(a.err, QE_ERR_TIMEOUT);
+      return;
     }
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-
-  // join the four warps: their o go through the ring's memory (each warp's
-  // ring holds its 16 x D floats), m and l through a small array
-  __shared__ float2 ml[kAttnWarps][16];
-  static_assert(kAttnStages<D> * 2 * kAttnTileBytes<D> >= 16 * D * 4, "ring holds a warp's output");
-  float* mine_o = reinterpret_cast<float*>(ring);
-  __syncwarp();
-  const int r = lane >> 2;
-#pragma unroll
-  for (int n = 0; n < D / 8; ++n) {
-    const int c = n * 8 + (lane & 3) * 2;
-    *reinterpret_cast<float2*>(mine_o + r * D + c) = make_float2(o[n][0], o[n][1]);
-    *reinterpret_cast<float2*>(mine_o + (r + 8) * D + c) = make_float2(o[n][2], o[n][3]);
-  }
-  if ((lane & 3) == 0) {
-    ml[warp][r] = make_float2(m0, l0);
-    ml[warp][r + 8] = make_float2(m1, l1);
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < 16 * (D / 4); e += kAttnThreads) {
-    const int row = e / (D / 4), c = (e % (D / 4)) * 4;
-    const long long dst = row_dst(row);
-    if (dst < 0) continue;
-    float m = ml[0][row].x;
-#pragma unroll
-    for (int w = 1; w < kAttnWarps; ++w) m = fmaxf(m, ml[w][row].x);
-    const float base = m == -INFINITY ? 0.f : m;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
-      const float f = exp2f(ml[w][row].x - base);
-      const float4 x = *reinterpret_cast<const float4*>(smem + w * S * 2 * TB + (row * D + c) * 4);
-      acc.x = fmaf(f, x.x, acc.x);
-      acc.y = fmaf(f, x.y, acc.y);
-      acc.z = fmaf(f, x.z, acc.z);
-      acc.w = fmaf(f, x.w, acc.w);
-      l = fmaf(f, ml[w][row].y, l);
-    }
-    *reinterpret_cast<float4*>(po + dst * D + c) = acc;
-    if (c == 0) pml[dst] = make_float2(m, l);
   }
 }
 
-QE_DEV int block_sum(int v, int* tmp) {  // over kAttnThreads threads; every thread gets the sum
-  v = __reduce_add_sync(0xffffffffu, v);
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int s = 0;
-#pragma unroll
-  for (int w = 0; w < kAttnWarps; ++w) s += tmp[w];
-  __syncthreads();
-  return s;
+QE_DEV bool soft_vote(bool x) {  // over the softmax warps
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r) : "r"((uint32_t)x) : "memory");
+  return r != 0;
+}
+QE_DEV void soft_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+
+// ------------------------------------------------------------------- roles
+
+// A role's place in the ring of segments.
+struct Reader {
+  int at = 0;
+  uint32_t phase = 0;
+  // Copies the next segment; by every lane of a warp, or by one thread alone.
+  QE_DEV void next(Segment& x, Shared& sh, const AttnArgs& a, bool warp, bool one) {
+    wait_for(&sh.seg_full[at], phase, sh, a);
+    x = sh.seg[at];
+    if (*(volatile int*)&sh.abort) x.n = 0;  // the ring may hold anything now
+    if (warp) __syncwarp();
+    if (one) mbar_arrive(&sh.seg_empty[at]);
+    if (++at == kSegRing) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// One thread: the CTA's segments in order, prefix first.
+template <int D>
+QE_DEV void deal_out(const AttnArgs& a, const Deal& d, long long t, long long t1, int b, long long b_start, int cap, Shared& sh) {
+  constexpr int max_rows = Shape<D>::kRows;
+  const int c = blockIdx.x, per = a.n_kv * a.rb_own;
+  int at = 0;
+  uint32_t phase = 1;
+  auto put = [&](const Segment& x) {
+    wait_for(&sh.seg_empty[at], phase, sh, a);
+    sh.seg[at] = x;
+    mbar_arrive(&sh.seg_full[at]);
+    if (++at == kSegRing) {
+      at = 0;
+      phase ^= 1;
+    }
+  };
+  Segment x;
+  if (c < d.grouped) {
+    const bool many = d.R > d.grid;
+    const int g = many ? 0 : c / d.R;
+    const long long s0 = d.group_start(g), s1 = d.group_start(g + 1);
+    x.list = a.prefix_pages;
+    x.kend = a.prefix_len;
+    x.b = -1;
+    for (int rb = many ? c : c - g * d.R; rb < d.R; rb += many ? d.grid : d.R) {
+      x.row0 = rb * max_rows;
+      x.rows = min(max_rows, a.B * a.G - x.row0);
+      long long s = s0;
+      x.h = (int)(s / a.prefix_tiles);
+      int i = (int)(s - (long long)x.h * a.prefix_tiles);
+      while (s < s1) {
+        x.n = (int)min((long long)(a.prefix_tiles - i), s1 - s);
+        x.key0 = i * kTile;
+        x.slot = g + x.h;
+        if (rb == 0) {
+          if (i == 0) a.prefix_groups[x.h].x = g;
+          if (i + x.n == a.prefix_tiles) a.prefix_groups[x.h].y = g;
+        }
+        put(x);
+        s += x.n;
+        i = 0;
+        ++x.h;
+      }
+    }
+  }
+  if (t < t1) {
+    int len = max(0, min(a.kv_len[b], cap)), nt = (len + kTile - 1) / kTile;
+    int unit = (int)((t - b_start) / nt), i = (int)(t - b_start - (long long)unit * nt);
+    for (;;) {
+      x.n = (int)min((long long)(nt - i), t1 - t);
+      x.h = unit / a.rb_own;
+      x.list = a.table + (size_t)b * a.table_stride;
+      x.key0 = i * kTile;
+      x.kend = len;
+      x.b = b;
+      x.row0 = (unit - x.h * a.rb_own) * max_rows;
+      x.rows = min(max_rows, a.G - x.row0);
+      const int u = b * per + unit;
+      x.slot = c + u;
+      if (i == 0) a.own_ctas[u].x = c;
+      if (i + x.n == nt) a.own_ctas[u].y = c;
+      put(x);
+      t += x.n;
+      if (t >= t1) break;
+      i = 0;
+      if (++unit == per) {
+        unit = 0;
+        do {
+          ++b;
+          len = max(0, min(a.kv_len[b], cap));
+        } while (len == 0 && b < a.B - 1);
+        nt = max(1, (len + kTile - 1) / kTile);
+      }
+    }
+  }
+  x.n = 0;
+  put(x);
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kAttnThreads) qe_attn_part_kernel(const AttnArgs a) {
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int tmp[kAttnWarps];
-  __shared__ int found[3];  // row, chunk within it, first chunk
+QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned char* qs) {
+  using Sh = Shape<D>;
+  constexpr int CH = Sh::kDims / 8;   // 16-byte pieces of a row of a stage
+  constexpr int RPI = 32 / CH;        // rows a warp instruction copies
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftWarps;
+  const int sub = lane % CH, sub_row = lane / CH;
+  // where this lane's piece of row 32 w + r goes, r = RPI i + sub_row: a swizzle of
+  // the row's low three bits, which are sub_row's and i's
+  const uint32_t ring_u = smem_u32(ring) + (sub >> 3) * (kTile * 128) + (32 * w + sub_row) * 128;
+  const uint32_t q_u = smem_u32(qs);
+  int stage = 0, phase = 1;  // fresh empty barriers count as free
+  Reader reader;
+  Segment x;
+  int left = 0, key0 = 0, n = 0, seg = -1, rows_before = 0;
+  auto page_at = [&](int first) {
+    const int key = first + 32 * w + lane;
+    return key < x.kend ? __ldg(x.list + a.page.div((uint32_t)key)) : -1;
+  };
+  const T *k_row = nullptr, *v_row = nullptr, *v_next = nullptr;
+  uint32_t live = 0, v_live = 0;
+  bool more = true;
+  while (true) {
+    // the next tile's keys
+    if (more && left == 0) {
+      reader.next(x, sh, a, true, lane == 0);
+      left = x.n;
+      key0 = x.key0;
+      more = left > 0;
+      if (more) {
+        // the block's queries, with its first tile's keys: two buffers for blocks of
+        // up to half the rows, the whole for larger ones
+        ++seg;
+        const bool wide = x.rows > Sh::kRows / 2 || rows_before > Sh::kRows / 2;
+        if (seg >= 2) wait_for(&sh.q_done[seg & 1], ((seg >> 1) - 1) & 1, sh, a);
+        if (seg >= 1 && wide) wait_for(&sh.q_done[(seg - 1) & 1], ((seg - 1) >> 1) & 1, sh, a);
+        __syncwarp();
+        rows_before = x.rows;
+        const int n16 = (x.rows + 15) & ~15;
+        const uint32_t dst = q_u + (x.rows <= Sh::kRows / 2 && (seg & 1) ? Sh::kRows / 2 * 128 : 0);
+#pragma unroll 1
+        for (int e = threadIdx.x - 32 * kSoftWarps; e < n16 * (D / 8); e += 32 * kProdWarps) {
+          const int r = e / (D / 8), ch = e % (D / 8);
+          const T* src = (const T*)a.q;
+          if (r < x.rows) {
+            const int f = x.row0 + r;
+            src += x.b >= 0 ? (size_t)x.b * a.q_stride + (size_t)(x.h * a.G + f) * D
+                            : (size_t)(f / a.G) * a.q_stride + (size_t)(x.h * a.G + f % a.G) * D;
+          }
+          cp_async16z(dst + (ch >> 3) * (Sh::kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + ch * 8, r < x.rows);
+        }
+      }
+    }
+    if (more) {
+      const int key = key0 + 32 * w + lane, page = page_at(key0);
+      const bool ok = page >= 0 && page < a.n_pages;
+      if (key < x.kend && !ok) set_error(a.err, QE_ERR_INVALID_ARG);
+      live = __ballot_sync(0xffffffffu, ok);
+      const long long in_page = ((long long)x.h * a.page.d + (key - (int)a.page.div((uint32_t)key) * (int)a.page.d)) * D;
+      k_row = (const T*)a.kc + (ok ? page * a.k_page_stride + in_page : 0);
+      v_next = (const T*)a.vc + (ok ? page * a.v_page_stride + in_page : 0);
+      if (lane == 0) sh.live[n & 7][w] = live;
+    }
+    // K of this tile, then V of the one before
+#pragma unroll 1
+    for (int p = more ? 0 : Sh::kParts; p < (n > 0 ? 2 : 1) * Sh::kParts; ++p) {
+      const bool is_v = p >= Sh::kParts;
+      const unsigned long long row = (unsigned long long)(is_v ? v_row : k_row) +
+                                     2 * ((is_v ? p - Sh::kParts : p) * Sh::kDims);
+      const uint32_t lv = is_v ? v_live : live;
+      wait_for(&sh.empty[stage], phase, sh, a);
+      __syncwarp();
+      const uint32_t dst = ring_u + stage * Sh::kStage;
+#pragma unroll
+      for (int i = 0; i < 32 / RPI; ++i) {
+        const int r = i * RPI + sub_row;
+        const unsigned long long at = __shfl_sync(0xffffffffu, row, r);
+        cp_async16z(dst + i * RPI * 128 + (((sub & 7) ^ (r & 7)) << 4), (const T*)at + sub * 8, (lv >> r) & 1);
+      }
+      // every lane's copies arrive when they land; lane 0 arrives for what it wrote itself
+      cp_async_mbar_arrive_noinc(&sh.full[stage]);
+      if (lane == 0) mbar_arrive(&sh.full[stage]);
+      if (++stage == Sh::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (!more) break;
+    v_row = v_next;
+    v_live = live;
+    key0 += kTile;
+    --left;
+    ++n;
+  }
+  cp_async_wait_all();
+}
+
+template <typename T, int D>
+QE_DEV void multiply(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned char* qs, unsigned char* ps,
+                     uint32_t tmem) {
+  using Sh = Shape<D>;
+  const uint32_t ring_u = smem_u32(ring), q_u = smem_u32(qs), p_u = smem_u32(ps);
+  int stage = 0, phase = 0;
+  auto take = [&]() {
+    wait_for(&sh.full[stage], phase, sh, a);
+    fence_async_smem();  // the copies wrote through the generic proxy, the products read through the async one
+    tc_after();
+    return ring_u + stage * Sh::kStage;
+  };
+  auto give = [&]() {
+    mma_commit(&sh.empty[stage]);
+    if (++stage == Sh::kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  };
+  Reader reader;
+  Segment x;
+  int left = 0, seg = -1;               // of the scores
+  int o_n16 = 0, o_seg = 0;             // of the outputs, one tile behind
+  bool o_first = false, more = true;
+  for (int n = 0;; ++n) {
+    bool first = false;
+    if (more && left == 0) {
+      reader.next(x, sh, a, false, true);
+      left = x.n;
+      more = left > 0;
+      first = true;
+      ++seg;
+    }
+    const int n16 = (x.rows + 15) & ~15;
+    if (more) {
+      const uint32_t idesc = mma_idesc<T>(n16, false);
+      const uint32_t q_at = desc_low(q_u + (x.rows <= Sh::kRows / 2 && (seg & 1) ? Sh::kRows / 2 * 128 : 0), 16);
+      const uint32_t d = tmem + (n & 1) * 128;
+#pragma unroll 1
+      for (int p = 0; p < Sh::kParts; ++p) {
+        const uint32_t k_at = desc_low(take(), 16), qp = q_at + p * (Sh::kDims / 64) * (Sh::kRows * 128 / 16);
+#pragma unroll
+        for (int k = 0; k < Sh::kDims / 16; ++k)
+          mma_issue(d, k_at + (k >> 2) * (kTile * 128 / 16) + (k & 3) * 2, qp + (k >> 2) * (Sh::kRows * 128 / 16) + (k & 3) * 2,
+                    idesc, p > 0 || k > 0);
+        give();
+      }
+      mma_commit(&sh.s_full[n & 1]);
+      if (--left == 0) mma_commit(&sh.q_done[seg & 1]);
+    }
+    if (n > 0) {  // the outputs of tile n - 1
+      const int m = n - 1;
+      if (o_first && o_seg >= 2) wait_for(&sh.o_free[o_seg & 1], ((o_seg >> 1) - 1) & 1, sh, a);
+      wait_for(&sh.p_full[m & 1], (m >> 1) & 1, sh, a);
+      const uint32_t idesc = mma_idesc<T>(o_n16, true);
+      const uint32_t d = tmem + 256 + (o_seg & 1) * 128;
+      const uint32_t p_at = desc_low(p_u + (o_n16 <= 64 && (m & 1) ? Sh::kP / 2 : 0), kTile * 128);
+#pragma unroll 1
+      for (int p = 0; p < Sh::kParts; ++p) {
+        // head_dim 64: the second 64 dims repeat the first (leading offset 0); they are not read
+        const uint32_t v_at = desc_low(take(), D == 64 ? 0 : kTile * 128);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_issue(d + p * 64, v_at + k * (2048 / 16), p_at + k * (2048 / 16), idesc, !o_first || k > 0);
+        give();
+      }
+      mma_commit(&sh.p_free[m & 1]);
+    }
+    if (!more) break;
+    o_n16 = n16;
+    o_seg = seg;
+    o_first = first;
+  }
+  // whatever happened, nothing is in flight when this returns
+  mma_commit(&sh.drained);
+  const uint64_t deadline = gtimer() + a.budget_ns;
+  while (!mbar_try_wait_sleep(&sh.drained, 0, 10000u))
+    if (gtimer() > deadline) {
+      set_error(a.err, QE_ERR_TIMEOUT);
+      break;
+    }
+}
+
+template <typename T, int D>
+QE_DEV void soften(const AttnArgs& a, Shared& sh, unsigned char* ps, uint32_t tmem_base) {
+  using Sh = Shape<D>;
+  constexpr int J = Sh::kRows / 32;  // most batches of 16 columns a thread has
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, side = threadIdx.x >> 7;
+  const int key = 32 * w + lane;
+  const uint32_t tmem = tmem_base + ((uint32_t)(32 * w) << 16);
+  float l[J][16];
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) l[j][e] = 0.f;
+  int seg = -1, left = 0;
+  bool wide = false, wide_before = false;  // more than 64 rows: P takes both buffers
+  Reader reader;
+  Segment x;
+  for (int n = 0;; ++n) {
+    bool first = false;
+    if (left == 0) {
+      reader.next(x, sh, a, true, lane == 0);
+      // the warps have to go through the same barriers: they end together
+      if (soft_vote(x.n == 0)) break;
+      left = x.n;
+      first = true;
+      ++seg;
+    }
+    const int nb = (x.rows + 15) >> 4;
+    wide_before = wide;
+    wide = nb > 4;
+    const uint32_t s_at = tmem + (n & 1) * 128, o_at = tmem + 256 + (seg & 1) * 128;
+    wait_for(&sh.s_full[n & 1], (n >> 1) & 1, sh, a);
+    __syncwarp();
+    tc_after();
+    const bool live = (sh.live[n & 7][w] >> lane) & 1;
+    float p[J][16];
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (2 * j + side < nb) tmem_ld16(s_at + (2 * j + side) * 16, p[j]);
+#pragma unroll
+      for (int j = 0; j < J; ++j) tmem_wait_ld(p[j]);
+      float most = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (2 * j + side < nb) {
+          const float4* ref = reinterpret_cast<const float4*>(sh.neg_ref + (2 * j + side) * 16);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 r = ref[e / 4];
+            p[j][e] = fmaf(p[j][e], a.scale_log2, r.x);
+            p[j][e + 1] = fmaf(p[j][e + 1], a.scale_log2, r.y);
+            p[j][e + 2] = fmaf(p[j][e + 2], a.scale_log2, r.z);
+            p[j][e + 3] = fmaf(p[j][e + 3], a.scale_log2, r.w);
+          }
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if (!live) p[j][e] = -INFINITY;
+            top[e & 3] = fmaxf(top[e & 3], p[j][e]);
+            p[j][e] = exp2_approx(p[j][e]);
+          }
+          most = fmaxf(most, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+        }
+      if (pass > 0 || !soft_vote(most > kSlack)) break;
+      // raise the references to the maxima so far; no product reads ps or writes o meanwhile
+      if (n > 1) wait_for(&sh.p_free[n & 1], ((n >> 1) - 1) & 1, sh, a);
+      if (n > 0) wait_for(&sh.p_free[(n - 1) & 1], ((n - 1) >> 1) & 1, sh, a);
+      __syncwarp();
+      tc_after();
+      float* scratch = reinterpret_cast<float*>(ps);
+#pragma unroll 1
+      for (int bb = side; bb < nb; bb += 2) {
+        float v[16];
+        __syncwarp();
+        tmem_ld16(s_at + bb * 16, v);
+        tmem_wait_ld(v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = live ? v[e] * a.scale_log2 : -INFINITY;
+        const float m = warp_reduce_rows_max<16>(v, lane);
+        if ((lane & 1) == 0) scratch[w * 128 + bb * 16 + reduced_row_of_lane<16>(lane)] = m;
+      }
+      soft_sync();
+      if (threadIdx.x < nb * 16) {
+        const int col = threadIdx.x;
+        const float old = -sh.neg_ref[col];
+        const float m = fmaxf(fmaxf(fmaxf(scratch[col], scratch[128 + col]), fmaxf(scratch[256 + col], scratch[384 + col])), old);
+        sh.neg_ref[col] = -m;
+        sh.factor[col] = exp2_approx(old - m);
+      }
+      soft_sync();
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (2 * j + side < nb) {
+          const float4* f = reinterpret_cast<const float4*>(sh.factor + (2 * j + side) * 16);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 r = f[e / 4];
+            l[j][e] *= r.x;
+            l[j][e + 1] *= r.y;
+            l[j][e + 2] *= r.z;
+            l[j][e + 3] *= r.w;
+          }
+        }
+      if (!first) {
+#pragma unroll 1
+        for (int i = side; i < nb * Sh::kParts; i += 2) {
+          const int bb = i % nb, d = i / nb;
+          float o[16];
+          const uint32_t at = o_at + d * 64 + bb * 16;
+          __syncwarp();
+          tmem_ld16(at, o);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] *= sh.factor[bb * 16 + e];
+          tmem_st16(at, o);
+        }
+        tmem_wait_st();
+      }
+      __syncwarp();
+    }
+    // the P that was in this place has been read
+    if (n > 1) wait_for(&sh.p_free[n & 1], ((n >> 1) - 1) & 1, sh, a);
+    if (n > 0 && (wide || wide_before)) wait_for(&sh.p_free[(n - 1) & 1], ((n - 1) >> 1) & 1, sh, a);
+    __syncwarp();
+    unsigned char* p_row = ps + (!wide && (n & 1) ? Sh::kP / 2 : 0) + key * Sh::kPRow;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (2 * j + side < nb) {
+        const int bb = 2 * j + side;
+        const int c = (bb & 3) * 2;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float* v = p[j] + 8 * hf;
+          *reinterpret_cast<uint4*>(p_row + (bb >> 2) * (kTile * 128) + (((c + hf) ^ (key & 7)) << 4)) =
+              make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) l[j][e] += p[j][e];
+      }
+    fence_async_smem();
+    tc_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.p_full[n & 1]);
+    if (--left > 0) continue;
+
+    // the segment's results
+    if (n > 0) wait_for(&sh.p_free[(n - 1) & 1], ((n - 1) >> 1) & 1, sh, a);
+    wait_for(&sh.p_free[n & 1], (n >> 1) & 1, sh, a);
+    __syncwarp();
+    tc_after();
+    float* scratch = reinterpret_cast<float*>(ps);
+    const size_t row_at = x.b >= 0 ? (size_t)x.slot * a.own_rows : (size_t)x.slot * a.B * a.G + x.row0;
+    float* po = (x.b >= 0 ? a.part_own : a.part_prefix) + row_at * D + key;
+    float2* pml = (x.b >= 0 ? a.ml_own : a.ml_prefix) + row_at;
+#pragma unroll 1
+    for (int i = side; i < nb * Sh::kParts; i += 2) {
+      const int bb = i % nb, d = i / nb;
+      float o[16];
+      __syncwarp();
+      tmem_ld16(o_at + d * 64 + bb * 16, o);
+      tmem_wait_ld(o);
+      if (D >= 128 || key < D) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (bb * 16 + e < x.rows) po[(size_t)(bb * 16 + e) * D + d * 128] = o[e];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (2 * j + side < nb) {
+        const float sum = warp_reduce_rows<16>(l[j], lane);
+        if ((lane & 1) == 0) scratch[w * 128 + (2 * j + side) * 16 + reduced_row_of_lane<16>(lane)] = sum;
+      }
+    tc_before();
+    soft_sync();
+    if (threadIdx.x < x.rows) {
+      const int col = threadIdx.x;
+      pml[col] = make_float2(-sh.neg_ref[col], (scratch[col] + scratch[128 + col]) + (scratch[256 + col] + scratch[384 + col]));
+    }
+    if (threadIdx.x < 128) sh.neg_ref[threadIdx.x] = kNoRef;
+    soft_sync();
+    if (lane == 0) mbar_arrive(&sh.o_free[seg & 1]);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) l[j][e] = 0.f;
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kAttnThreads, 1) qe_attn_part_kernel(const __grid_constant__ AttnArgs a) {
+  using Sh = Shape<D>;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(16) Shared sh;
+  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  unsigned char *ring = smem, *qs = smem + Sh::kStages * Sh::kStage, *ps = qs + Sh::kQ;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Sh::kStages; ++i) {
+      mbar_init(&sh.full[i], kProdWarps * 33);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], kSoftWarps);
+      mbar_init(&sh.p_free[i], 1);
+      mbar_init(&sh.q_done[i], 1);
+      mbar_init(&sh.o_free[i], kSoftWarps);
+    }
+    for (int i = 0; i < kSegRing; ++i) {
+      mbar_init(&sh.seg_full[i], 1);
+      mbar_init(&sh.seg_empty[i], kSegReaders);
+    }
+    mbar_init(&sh.drained, 1);
+    fence_mbar_init();
+    sh.abort = 0;
+  }
+  if (threadIdx.x < 128) sh.neg_ref[threadIdx.x] = kNoRef;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int n_prefix = a.nsp * a.n_kv * a.rb_prefix;
-  int item = blockIdx.x;
-  if (item < n_prefix) {
-    const int rb = item % a.rb_prefix;
-    const int h = item / a.rb_prefix % a.n_kv;
-    const int s = item / (a.rb_prefix * a.n_kv);
-    const int k0 = s * a.prefix_chunk, k1 = min(a.prefix_len, k0 + a.prefix_chunk);
-    const int rows = a.B * a.G;
-    auto src = [&](int i) -> const void* {
-      const int f = rb * 16 + i;
-      return f < rows ? (const T*)a.q + (size_t)(f / a.G) * a.q_stride + (size_t)(h * a.G + f % a.G) * D : nullptr;
-    };
-    auto dst = [&](int i) -> long long {
-      const int f = rb * 16 + i;
-      return f < rows ? (long long)(f / a.G) * a.n_q + h * a.G + f % a.G : -1;
-    };
-    const size_t base = (size_t)s * a.B * a.n_q;
-    attn_chunk<T, D>(a, h, a.prefix_pages, k0, k1, src, dst, a.part_prefix + base * D, a.ml_prefix + base, smem);
-    return;
-  }
-  item -= n_prefix;
-  // the rows' own keys: chunks of one length for the whole batch
+
+  // the total of own tiles, then the batch row in which this CTA's share starts
   const int cap = (int)min((long long)a.table_stride * a.page.d, 1ll << 30);
-  auto len_of = [&](int b) { return b < a.B ? max(0, min(a.kv_len[b], cap)) : 0; };
-  long long total = 0;
   const int per = a.n_kv * a.rb_own;
-  {
-    // 64-bit total of lengths: sums of 16 bits each side of the word
-    int lo = 0, hi = 0;
-    for (int b = threadIdx.x; b < a.B; b += kAttnThreads) {
-      const int n = len_of(b);
-      lo += n & 0x7fff;
-      hi += n >> 15;
-    }
-    total = (long long)block_sum(lo, tmp) + ((long long)block_sum(hi, tmp) << 15);
-  }
-  const long long want = (total * per + a.own_target - 1) / a.own_target;
-  const int chunk = (int)(((want < 1 ? 1 : want) + 63) / 64 * 64);
-  const int j = item / per, hr = item % per;
-  // the row that chunk j belongs to
-  int before = 0;
-  bool have = false;
-  for (int b0 = 0; b0 < a.B && !have; b0 += kAttnThreads) {
-    const int b = b0 + threadIdx.x;
-    const int n = (len_of(b) + chunk - 1) / chunk;
-    int scan = n;
+  auto tiles_of = [&](int b) { return b < a.B ? (max(0, min(a.kv_len[b], cap)) + kTile - 1) / kTile : 0; };
+  // inclusive sums over the CTA's threads; the total in sh.sum[16]
+  auto block_scan = [&](long long v) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, scan, d);
-      if ((threadIdx.x & 31) >= d) scan += x;
+      const long long u = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += u;
     }
-    if ((threadIdx.x & 31) == 31) tmp[threadIdx.x >> 5] = scan;
     __syncthreads();
-    int sum = 0;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
-      if (w < (int)(threadIdx.x >> 5)) scan += tmp[w];
-      sum += tmp[w];
-    }
-    const int first = before + scan - n;
-    if (n > 0 && j >= first && j < first + n) {
-      found[0] = b;
-      found[1] = j - first;
-      found[2] = first;
-    }
-    before += sum;
-    have = j < before;
+    if (lane == 31) sh.sum[warp] = v;
     __syncthreads();
-  }
-  if (!have) return;
-  const int b = found[0], ci = found[1];
-  const int len = len_of(b), h = hr / a.rb_own, rb = hr % a.rb_own;
-  if (threadIdx.x == 0 && ci == 0 && hr == 0) {
-    a.own_info[b] = make_int2(found[2], (len + chunk - 1) / chunk);
-    if (a.kv_len[b] > cap) set_error(a.err, QE_ERR_INVALID_ARG);
-  }
-  const int k0 = ci * chunk, k1 = min(len, k0 + chunk);
-  auto src = [&](int i) -> const void* {
-    const int g = rb * 16 + i;
-    return g < a.G ? (const T*)a.q + (size_t)b * a.q_stride + (size_t)(h * a.G + g) * D : nullptr;
+    long long all = 0;
+#pragma unroll 1
+    for (int i = 0; i < kAttnThreads / 32; ++i) {
+      if (i == warp) v += all;
+      all += sh.sum[i];
+    }
+    return make_longlong2(v, all);
   };
-  auto dst = [&](int i) -> long long {
-    const int g = rb * 16 + i;
-    return g < a.G ? (long long)h * a.G + g : -1;
-  };
-  const size_t base = (size_t)j * a.n_q;
-  attn_chunk<T, D>(a, h, a.table + (size_t)b * a.table_stride, k0, k1, src, dst, a.part_own + base * D,
-                   a.ml_own + base, smem);
+  long long mine = 0;
+  for (int b = threadIdx.x; b < a.B; b += kAttnThreads) {
+    mine += tiles_of(b);
+    if (blockIdx.x == 0 && a.kv_len[b] > cap) set_error(a.err, QE_ERR_INVALID_ARG);
+  }
+  const longlong2 sums = block_scan(mine);
+  const Deal deal(a, sums.y * per);
+  const long long t0 = deal.own_start(blockIdx.x), t1 = deal.own_start(blockIdx.x + 1);
+  if (threadIdx.x == 0) {
+    a.own_start[blockIdx.x] = t0;
+    if (blockIdx.x == gridDim.x - 1) a.own_start[gridDim.x] = deal.own;
+  }
+  if (t0 == t1 && blockIdx.x >= deal.grouped) return;  // uniform over the CTA
+  if (warp == 12) {
+    __syncwarp();
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    tc_before();
+  }
+  if (t0 < t1) {
+    long long before = 0;  // tiles of the rows of earlier passes, per key head and row block
+    for (int b0 = 0; b0 < a.B && before * per <= t0; b0 += kAttnThreads) {
+      const int b = b0 + threadIdx.x, nt = tiles_of(b);
+      const longlong2 scan = block_scan(nt);
+      const long long end = (before + scan.x) * per, start = end - (long long)nt * per;
+      if (start <= t0 && t0 < end) {
+        sh.found = b;
+        sh.found_start = start;
+      }
+      before += scan.y;
+    }
+  }
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *(volatile uint32_t*)&sh.tmem;
+  if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    soften<T, D>(a, sh, ps, tmem);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp < kSoftWarps + kProdWarps) {
+      produce<T, D>(a, sh, ring, qs);
+    } else if (warp == 12) {
+      if (lane == 0) multiply<T, D>(a, sh, ring, qs, ps, tmem);
+      __syncwarp();
+    } else if (warp == 13) {
+      if (lane == 0) deal_out<D>(a, deal, t0, t1, sh.found, sh.found_start, cap, sh);
+      __syncwarp();
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 12) {
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
 }
 
-// Joins the chunks of each row: one warp a row, prefix chunks first, then own.
-template <typename T, int D>
-__global__ void __launch_bounds__(kAttnThreads) qe_attn_join_kernel(const AttnArgs a) {
+// Joins the segments of each row, prefix first, then own, in the order of their
+// CTAs.  WPR warps take a row's segments in turn and are added up in order.
+template <typename T, int D, int WPR>
+__global__ void __launch_bounds__(128) qe_attn_join_kernel(const __grid_constant__ AttnArgs a) {
+  __shared__ float sh_l[4];
+  __shared__ float sh_o[4][D];
+  constexpr int max_rows = Shape<D>::kRows;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kAttnWarps + (threadIdx.x >> 5);
-  const long long rows = (long long)a.B * a.n_q;
-  if (row >= rows) return;
-  const int b = (int)(row / a.n_q), hq = (int)(row % a.n_q);
-  const int kv = a.kv_len[b];
-  if (kv < 0) return;
-  const bool own = kv > 0 && a.table_stride > 0;
-  if (kv > 0 && !own && lane == 0) set_error(a.err, QE_ERR_INVALID_ARG);
-  const int2 info = own ? a.own_info[b] : make_int2(0, 0);
-  const int n = a.nsp + info.y;
-  auto at = [&](int i) { return i < a.nsp ? (size_t)i * rows + row : (size_t)(info.x + i - a.nsp) * a.n_q + hq; };
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, (i < a.nsp ? a.ml_prefix : a.ml_own)[at(i)].x);
-  m = warp_max(m);
-  const float base = m == -INFINITY ? 0.f : m;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp % WPR;
+  const int rows = a.B * a.n_q, row = blockIdx.x * (4 / WPR) + warp / WPR;
+  const bool real = row < rows;
+  const int b = real ? row / a.n_q : 0, hq = row - b * a.n_q, h = hq / a.G, g = hq - h * a.G;
+  const int kv = real ? a.kv_len[b] : -1;
+  int g0 = 0, np = 0, c0 = 0, no = 0;  // first group and CTA that hold segments, and how many
+  if (kv >= 0 && a.prefix_tiles > 0) {
+    const int2 r = a.prefix_groups[h];
+    g0 = r.x;
+    np = r.y - r.x + 1;
+  }
+  const int unit = (b * a.n_kv + h) * a.rb_own + g / max_rows;
+  if (kv > 0 && a.table_stride > 0) {
+    const int2 r = a.own_ctas[unit];
+    c0 = r.x;
+    no = r.y - r.x + 1;
+  }
+  // segment i of this row: offset of its row, or of the first row of all if the CTA had no own tiles
+  auto where = [&](int i, const float2** ml, const float** o) {
+    size_t at;
+    if (i < np) {
+      at = (size_t)(g0 + i + h) * a.B * a.G + (size_t)b * a.G + g;
+      *ml = a.ml_prefix + at;
+      *o = a.part_prefix + at * D;
+      return true;
+    }
+    const int c = c0 + i - np;
+    at = (size_t)(c + unit) * a.own_rows + g % max_rows;
+    *ml = a.ml_own + at;
+    *o = a.part_own + at * D;
+    return a.own_start[c] < a.own_start[c + 1];
+  };
   constexpr int E = D / 32;
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  float l = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const int i = i0 + lane;
-    float f = 0.f;
-    if (i < n) {
-      const float2 ml = (i < a.nsp ? a.ml_prefix : a.ml_own)[at(i)];
-      f = exp2f(ml.x - base);
-      l = fmaf(f, ml.y, l);
+  float m = -kNoRef, l = 0.f;
+  // segments share, share + WPR, ... of this row, 32 in a pass: lane k has the k-th's m and l
+#pragma unroll 1
+  for (int i0 = share; i0 < np + no; i0 += 32 * WPR) {
+    const int i = i0 + lane * WPR;
+    float2 ml = make_float2(-kNoRef, 0.f);
+    const float* o = nullptr;
+    bool has = false;
+    if (i < np + no) {
+      const float2* p;
+      has = where(i, &p, &o);
+      if (has) ml = *p;
     }
-    const int lim = min(32, n - i0);
-#pragma unroll 4
-    for (int k = 0; k < lim; ++k) {
-      const float w = __shfl_sync(0xffffffffu, f, k);
-      const int ik = i0 + k;
-      const float* p = (ik < a.nsp ? a.part_prefix : a.part_own) + at(ik) * D + lane * E;
+    const float top = fmaxf(m, warp_max(ml.x)), f0 = exp2_approx(m - top), f = has ? exp2_approx(ml.x - top) : 0.f;
+    m = top;
+    l = fmaf(f, ml.y, l * f0);  // per lane
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, p[e], acc[e]);
+    for (int e = 0; e < E; ++e) acc[e] *= f0;
+    const int n = min(32, (np + no - i0 + WPR - 1) / WPR);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float w = __shfl_sync(0xffffffffu, f, k);
+      const float* p = (const float*)__shfl_sync(0xffffffffu, (unsigned long long)(has ? o : nullptr), k);
+      if (!p) continue;
+      float v[E];
+      if constexpr (E == 2) {
+        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(p + lane * E);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(p + lane * E + e);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e]);
     }
   }
   l = warp_sum(l);
+  if constexpr (WPR > 1) {
+    if (lane == 0) sh_l[warp] = m;
+    __syncthreads();
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < WPR; ++i) top = fmaxf(top, sh_l[i]);
+    const float f = exp2_approx(m - top);
+    m = top;
+    __syncthreads();
+    if (lane == 0) sh_l[warp] = l * f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sh_o[warp][lane * E + e] = acc[e] * f;
+    __syncthreads();
+    if (share != 0) return;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < WPR; ++i) {
+      l += sh_l[i];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += sh_o[i][lane * E + e];
+    }
+  }
+  if (kv < 0) return;
+  if (kv > 0 && a.table_stride == 0 && lane == 0) set_error(a.err, QE_ERR_INVALID_ARG);
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN sum stays one
   uint32_t* out = reinterpret_cast<uint32_t*>((T*)a.out + (size_t)b * a.out_stride + (size_t)hq * D + lane * E);
 #pragma unroll
   for (int e = 0; e < E; e += 2) out[e / 2] = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
-  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.69314718055994531f;
+  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 // Sizes that depend on the shape alone, whatever the lengths.
 struct AttnPlan {
-  int rb_own, rb_prefix, own_target, nsp_max, own_chunks_max;
-  size_t off_info, off_mlp, off_mlo, off_pp, off_po, total;
+  int grid, max_rows, rb_own, rb_prefix, own_rows, groups;
+  size_t off_cta, off_own, off_groups, off_mlp, off_mlo, off_pp, off_po, total;
 };
 AttnPlan attn_plan(int n_kv, int n_q, int D, int B, int sms) {
   AttnPlan p{};
   const int G = n_q / n_kv;
-  p.rb_own = (G + 15) / 16;
-  p.rb_prefix = (int)(((long long)B * G + 15) / 16);
-  p.own_target = 4 * sms;
-  p.nsp_max = 4 * sms / (n_kv * p.rb_prefix);
-  if (p.nsp_max < 1) p.nsp_max = 1;
-  p.own_chunks_max = p.own_target / (n_kv * p.rb_own) + 1 + B;
+  p.grid = sms;
+  p.max_rows = D == 256 ? Shape<256>::kRows : Shape<128>::kRows;
+  p.rb_own = (G + p.max_rows - 1) / p.max_rows;
+  p.rb_prefix = (B * G + p.max_rows - 1) / p.max_rows;
+  p.own_rows = G < p.max_rows ? G : p.max_rows;
+  // a segment's slot: its CTA (or group) plus its block's (or key head's) number
+  p.groups = p.rb_prefix <= p.grid ? p.grid / p.rb_prefix : 1;
+  const size_t rows_p = (size_t)(p.groups + n_kv) * B * G;
+  const size_t rows_o = ((size_t)p.grid + (size_t)B * n_kv * p.rb_own) * p.own_rows;
   size_t off = sizeof(WsControl);
   auto take = [&](size_t bytes) { const size_t o = off; off = (off + bytes + 255) & ~(size_t)255; return o; };
-  const size_t rows = (size_t)B * n_q;
-  p.off_info = take(sizeof(int2) * (size_t)B);
-  p.off_mlp = take(sizeof(float2) * p.nsp_max * rows);
-  p.off_mlo = take(sizeof(float2) * (size_t)p.own_chunks_max * n_q);
-  p.off_pp = take(4 * (size_t)p.nsp_max * rows * D);
-  p.off_po = take(4 * (size_t)p.own_chunks_max * n_q * D);
+  p.off_cta = take(8 * ((size_t)p.grid + 1));
+  p.off_own = take(sizeof(int2) * (size_t)B * n_kv * p.rb_own);
+  p.off_groups = take(sizeof(int2) * (size_t)n_kv);
+  p.off_mlp = take(sizeof(float2) * rows_p);
+  p.off_mlo = take(sizeof(float2) * rows_o);
+  p.off_pp = take(4 * rows_p * D);
+  p.off_po = take(4 * rows_o * D);
   p.total = off;
   return p;
 }
@@ -477,14 +991,14 @@ cudaError_t launch_attn_t(const AttnArgs& a, int grid, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!set[dev]) {
-    e = cudaFuncSetAttribute(qe_attn_part_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem<D>);
+    e = cudaFuncSetAttribute(qe_attn_part_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kAttnThreads);
-  cfg.dynamicSmemBytes = kAttnSmem<D>;
+  cfg.dynamicSmemBytes = Shape<D>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -493,9 +1007,16 @@ cudaError_t launch_attn_t(const AttnArgs& a, int grid, cudaStream_t s) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, qe_attn_part_kernel<T, D>, a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(((long long)a.B * a.n_q + kAttnWarps - 1) / kAttnWarps));
+  const long long rows = (long long)a.B * a.n_q;
+  cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, qe_attn_join_kernel<T, D>, a);
+  // few rows have many segments each: four warps a row; many rows have few
+  if (rows < 8ll * grid) {
+    cfg.gridDim = dim3((unsigned)rows);
+    return cudaLaunchKernelEx(&cfg, qe_attn_join_kernel<T, D, 4>, a);
+  }
+  cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+  return cudaLaunchKernelEx(&cfg, qe_attn_join_kernel<T, D, 1>, a);
 }
 
 template <typename T>
@@ -510,7 +1031,7 @@ int check_attn_shape(const qe_kv_cache* c, int n_q, int B) {
   if (rc) return rc;
   if (n_q < 1 || n_q > kMaxHeads || n_q % c->n_kv)
     return fail(QE_ERR_INVALID_ARG, "n_q must be a positive multiple of n_kv <= %d (got %d, n_kv %d)", kMaxHeads, n_q, c->n_kv);
-  if (B < 0 || B > kMaxRows) return fail(QE_ERR_INVALID_ARG, "B must be in [0, %d] (got %d)", kMaxRows, B);
+  if (B < 0 || B > kMaxBatch) return fail(QE_ERR_INVALID_ARG, "B must be in [0, %d] (got %d)", kMaxBatch, B);
   return QE_OK;
 }
 
@@ -557,32 +1078,22 @@ extern "C" QE_API int attn_decode_step(const qe_kv_cache* c, int B, int n_q, con
   a.k_page_stride = c->k_page_stride; a.v_page_stride = c->v_page_stride;
   a.prefix_pages = prefix_pages; a.table = table; a.kv_len = kv_len; a.lse = lse;
   a.err = &((WsControl*)ws)->err;
-  a.own_info = (int2*)(w + p.off_info);
+  a.own_start = (long long*)(w + p.off_cta);
+  a.own_ctas = (int2*)(w + p.off_own);
+  a.prefix_groups = (int2*)(w + p.off_groups);
   a.ml_prefix = (float2*)(w + p.off_mlp); a.ml_own = (float2*)(w + p.off_mlo);
   a.part_prefix = (float*)(w + p.off_pp); a.part_own = (float*)(w + p.off_po);
+  a.budget_ns = wait_budget_ns();
   a.B = B; a.n_q = n_q; a.n_kv = c->n_kv; a.G = n_q / c->n_kv; a.n_pages = c->n_pages;
   a.table_stride = table_stride; a.prefix_len = prefix_len;
-  a.rb_own = p.rb_own; a.rb_prefix = p.rb_prefix; a.own_target = p.own_target;
+  a.prefix_tiles = (prefix_len + kTile - 1) / kTile;
+  const long long line = (long long)a.prefix_tiles * c->n_kv;
+  a.groups = line > 0 && line < p.groups ? (int)line : p.groups;
+  a.rb_prefix = p.rb_prefix; a.rb_own = p.rb_own; a.own_rows = p.own_rows;
   a.scale_log2 = scale * kLog2e;
   a.page = fast_div((uint32_t)c->page_size);
-  if (prefix_len > 0) {
-    int nsp = (prefix_len + 127) / 128;
-    nsp = nsp > p.nsp_max ? p.nsp_max : nsp;
-    a.prefix_chunk = ((prefix_len + nsp - 1) / nsp + 63) / 64 * 64;
-    a.nsp = (prefix_len + a.prefix_chunk - 1) / a.prefix_chunk;
-  }
-  // own items: at most own_target plus one partial chunk for each row, key head and row block
-  long long own = 0;
-  if (table_stride > 0) {
-    const long long per = (long long)a.n_kv * a.rb_own;
-    const long long most = (long long)B * (((long long)table_stride * c->page_size + 63) / 64) * per;
-    own = (long long)p.own_chunks_max * per;
-    own = own < most ? own : most;
-  }
-  const long long grid = (long long)a.nsp * a.n_kv * a.rb_prefix + own;
-  if (grid > 0x7fffffffLL) return fail(QE_ERR_UNSUPPORTED, "attn_decode_step: too many parts");
-  const cudaError_t e = c->dtype == QE_BF16 ? launch_attn<__nv_bfloat16>(a, D, (int)grid, (cudaStream_t)stream)
-                                            : launch_attn<__half>(a, D, (int)grid, (cudaStream_t)stream);
+  const cudaError_t e = c->dtype == QE_BF16 ? launch_attn<__nv_bfloat16>(a, D, p.grid, (cudaStream_t)stream)
+                                            : launch_attn<__half>(a, D, p.grid, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "attn_decode_step launch");
   return QE_OK;
 }

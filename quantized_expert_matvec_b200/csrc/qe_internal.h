@@ -208,6 +208,7 @@ cudaError_t launch_gdn_step(long long n_heads, int dk, int dv, float* S, const f
                             const float* v, const float* alpha, const float* beta, float* o, int sms,
                             cudaStream_t s);
 
+unsigned long long wait_budget_ns();  // qe_set_wait_budget_ns's value
 int fail(int code, const char* fmt, ...);
 int cuda_fail(cudaError_t e, const char* what);
 int check_cfg(const qe_cfg* c);
