@@ -5,21 +5,27 @@
 //
 // over the prefix's keys, then row b's own.  The work is cut into tiles of 128
 // keys of one key head for a block of query rows: the group's heads of one batch
-// row (own keys), or up to 128 rows of the whole batch (prefix keys, which are
-// therefore read once for all of them).  A persistent CTA per SM takes an equal
-// share of the tiles, whatever the lengths; a run of tiles of one block within a
-// CTA is a segment.  A segment leaves, per query row, a reference m, the sum l of
-// 2^(s - m) (scores s in log2 units) and the output sum o of 2^(s - m) v;
-// the second kernel joins a row's segments in a fixed order:
+// row (own keys), or rows of the whole batch (prefix keys, which are therefore
+// read once for all of them).  A persistent CTA per SM takes an equal share of the
+// tiles, whatever the lengths; a run of tiles of one block within a CTA is a
+// segment.  A segment leaves, per query row, a reference m, the sum l of 2^(s - m)
+// (scores s in log2 units) and the output sum o of 2^(s - m) v; the second kernel
+// joins a row's segments in a fixed order:
 //   out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,   M = max m_i.
 //
-// Both products run on the tensor cores with the keys along M, so that a decode
-// step's few rows are a small N and not a padded M:
-//   S^T [128 keys x N]   = K [128 x D] Q^T     (K and Q as they lie: K-major)
-//   O^T [D x N]         += V^T [D x 128] P^T   (V and P as they lie: MN-major)
-// N is the number of rows rounded up to 16.  Accumulators are in tensor memory: two
-// of S^T, two of O^T.  Roles of the 16 warps:
-//   0-7   softmax: a thread has one key (lane of S^T) and the columns of every other 16;
+// Both products run on the tensor cores, accumulators in tensor memory.  Blocks of
+// up to 64 rows (narrow) have the keys along M, so that a decode step's few rows
+// are a small N and not a padded M:
+//   S^T [128 keys x N] = K [128 x D] Q^T     (as they lie: K-major)
+//   O^T [D x N]       += V^T [D x 128] P^T   (as they lie: MN-major; P in shared memory)
+// Larger blocks (wide: up to 256 rows, 128 at head_dim 256) have 128 rows along M:
+//   S [128 x 128 keys] = Q [128 x D] K^T
+//   O [128 x D]       += P [128 x 128] V     (P over S in tensor memory)
+// so that a softmax thread has a whole row and needs no other's.
+// Roles of the 16 warps:
+//   0-7   softmax, two groups of four: narrow segments alternate between them (the
+//         end of one overlaps the start of the next), a wide one's rows 0-127 and
+//         128-255 are one group's each;
 //   8-11  producers: K and V rows by cp.async from their pages into a ring of
 //         128-byte-swizzled tiles; keys that do not exist become zeros;
 //   12    one thread issues the products;
@@ -27,9 +33,9 @@
 //         (each role working them out for itself made the code 160 KB and every
 //         role wait for its instructions).
 // The reference m need not be the maximum: it is raised (and o, l rescaled) only
-// when a score passes it by more than 2^8, which one vote per tile finds.
-// l is the sum of the fp32 numerators; their rounding to the cache's dtype is
-// the one that the second product's operand type asks for.
+// when a score passes it by more than 2^8.  l is the sum of the fp32 numerators;
+// their rounding to the cache's dtype is the one that the second product's
+// operand type asks for.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -46,27 +52,36 @@ namespace {
 
 constexpr int kMaxBatch = 4096;  // B
 constexpr int kTile = 128;       // keys per tile
+constexpr int kNarrow = 64;      // most rows of a narrow block
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNoRef = 3.0e38f;  // -m before the first score
 constexpr float kSlack = 8.f;      // a score may pass the reference by this (log2)
+// A segment costs its CTA about one tile's time beside its tiles (queries, first
+// reference, results): the deal counts that in.
+constexpr int kSegmentCost = 1;
 
 constexpr int kSoftWarps = 8, kProdWarps = 4;
-constexpr int kAttnThreads = 512;  // 8 softmax, 4 producer, 1 product warp; 3 fill up the register split
+constexpr int kAttnThreads = 512;  // 8 softmax, 4 producer, product and dealing warps; 2 fill up the register split
 // registers a thread: 256 x 176 + 256 x 80 = 65536 = 512 x 128, the launch's
 constexpr int kSoftRegs = 176, kOtherRegs = 80;
+constexpr int kMaxStages = 10, kSegRing = 6;
+constexpr int kSegReaders = kSoftWarps + kProdWarps + 1;
 
 template <int D>
 struct Shape {
-  static constexpr int kRows = D == 256 ? 64 : 128;        // query rows per block (most N)
-  static constexpr int kParts = D == 256 ? 2 : 1;          // a K or V tile is this many stages
-  static constexpr int kDims = D / kParts;                 // dims per stage
-  static constexpr int kStage = kTile * kDims * 2;         // bytes
-  static constexpr int kQ = kRows * D * 2;
-  static constexpr int kPRow = 128;                        // bytes of a key's line of 64 rows of P
-  static constexpr int kP = 2 * kTile * 128;               // two blocks of 64 rows, or two buffers of one
+  static constexpr int kRows = D == 256 ? 128 : 256;  // query rows of a block at most
+  static constexpr int kParts = D == 256 ? 2 : 1;     // a K or V tile is this many stages
+  static constexpr int kDims = D / kParts;            // dims per stage
+  static constexpr int kStage = kTile * kDims * 2;    // bytes
   static constexpr int kStages = D == 64 ? 10 : 5;
-  static constexpr int kSmem = 1024 + kStages * kStage + kQ + kP;
+  // narrow queries: 128 (64) lines per 64 dims, two buffers of half of them each;
+  // narrow P: two buffers of 128 keys x 64 rows; wide queries take both places
+  static constexpr int kQLines = D == 256 ? 64 : 128;
+  static constexpr int kQ = kQLines * D * 2;
+  static constexpr int kP = kTile * kNarrow * 2;
+  static constexpr int kSmem = 1024 + kStages * kStage + kQ + 2 * kP;
   static_assert(kSmem + 2048 <= 232448, "shared memory of a CTA");
+  static_assert(kRows * D * 2 <= kQ + 2 * kP, "wide queries");
 };
 
 struct AttnArgs {
@@ -80,21 +95,22 @@ struct AttnArgs {
   const int32_t* kv_len;
   float* lse;
   int* err;
-  long long* own_start;  // [grid + 1] first own tile of each CTA
+  long long* own_start;  // [grid + 1] where each CTA's share of the own line starts
   int2* own_ctas;        // [own block] first and last CTA that work on it
   int2* prefix_groups;   // [key head] first and last group
-  float2* ml_prefix;     // [slot][B * G] {m, l}
-  float2* ml_own;        // [slot][rows of a block]
+  float2* ml_prefix;     // [slot][B * G][4] {m, part of l}
+  float2* ml_own;        // [slot][rows of a block][4]
   float* part_prefix;    // [slot][B * G][D]
   float* part_own;       // [slot][rows of a block][D]
   unsigned long long budget_ns;
   int B, n_q, n_kv, G, n_pages, table_stride, prefix_len;
-  int prefix_tiles;      // per key head
-  int groups;            // groups of CTAs, one CTA per row block, that share the prefix
-  int rb_prefix, rb_own; // row blocks per key head
-  int own_rows;          // rows of an own block: min(G, kRows)
+  int prefix_tiles;       // per key head
+  int prefix_cost;        // of a prefix tile, in narrow tiles
+  int groups;             // groups of CTAs, one CTA per row block, that share the prefix
+  int rb_prefix, rb_own;  // row blocks per key head
+  int own_rows;           // rows of an own block: min(G, kRows)
   float scale_log2;
-  FastDiv page;
+  FastDiv page, group;    // by the page size and by G
 };
 
 // ------------------------------------------------------------ tensor cores
@@ -108,9 +124,9 @@ constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 QE_DEV uint32_t desc_low(uint32_t addr, uint32_t lbo) { return ((addr & 0x3ffffu) >> 4) | ((lbo >> 4) << 16); }
 // Instruction descriptor, kind::f16: fp32 accumulator, both operands of T, M = 128.
 template <typename T>
-QE_DEV uint32_t mma_idesc(int N, bool mn_major) {
+QE_DEV uint32_t mma_idesc(int N, bool a_mn, bool b_mn) {
   const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-  return (1u << 4) | (type << 7) | (type << 10) | (mn_major ? (1u << 15) | (1u << 16) : 0u) |
+  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 QE_DEV void mma_issue(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
@@ -127,21 +143,29 @@ QE_DEV void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: 
 QE_DEV void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 QE_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// the same with A in tensor memory
+QE_DEV void mma_issue_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
+}
+
 // 16 columns of the warp's 32 lanes
 QE_DEV void tmem_ld16(uint32_t a, float (&v)[16]) {
-  uint32_t r[16];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
       : "r"(a));
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-QE_DEV void tmem_st16(uint32_t a, const float (&v)[16]) {
+template <typename U>
+QE_DEV void tmem_st16(uint32_t a, const U (&v)[16]) {
+  static_assert(sizeof(U) == 4, "32-bit columns");
   uint32_t r[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  for (int i = 0; i < 16; ++i) r[i] = *reinterpret_cast<const uint32_t*>(&v[i]);
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
@@ -169,38 +193,47 @@ QE_DEV void cp_async16z(uint32_t dst, const void* src, bool real) {
 
 // ------------------------------------------------------------------ shares
 
-// How the tiles are dealt out.  Prefix: `groups` groups of one CTA per row block,
-// so that a group reads the same keys at the same time; group g has the tiles
+// x * num / den, with 32-bit arithmetic where the product has 32 bits (a 64-bit
+// division takes about as long as a global load)
+QE_DEV long long mul_div(long long x, int num, int den) {
+  if (x < (1 << 20) && num < (1 << 11)) return (uint32_t)x * (uint32_t)num / (uint32_t)den;
+  return x * num / den;
+}
+
+// How the work is dealt out.  Prefix: `groups` groups of one CTA per row block, so
+// that a group reads the same keys at the same time; group g has the tiles
 // [g S / groups, (g + 1) S / groups) of the line (key head, tile) of length S.  More
 // row blocks than CTAs: one group, each CTA takes every grid-th block.  Own: a line
-// (batch row, key head, row block, tile) of which each CTA takes what brings its
-// total to an equal share.
+// (batch row, key head, row block, places), where a block has kSegmentCost places
+// more than tiles, of which each CTA takes what brings its total to an equal share.
 struct Deal {
-  int grid, R, groups, grouped;
+  int grid, R, groups, grouped, cost;
   long long S, own;
-  QE_DEV Deal(const AttnArgs& a, long long own_tiles) : grid(gridDim.x), R(a.rb_prefix), groups(a.groups), own(own_tiles) {
+  QE_DEV Deal(const AttnArgs& a, long long own_places)
+      : grid(gridDim.x), R(a.rb_prefix), groups(a.groups), cost(a.prefix_cost), own(own_places) {
     S = (long long)a.prefix_tiles * a.n_kv;
     grouped = S == 0 ? 0 : R <= grid ? groups * R : grid;
   }
-  QE_DEV long long group_start(int g) const { return S * g / groups; }
+  QE_DEV long long group_start(int g) const { return mul_div(S, g, groups); }
   QE_DEV long long own_start(int c) const {
     if (c >= grid) return own;
-    if (S == 0) return own * c / grid;
-    const long long total = own + S * R, each = (S + groups - 1) / groups;
-    if (R <= grid && total / grid >= each) {  // every CTA has room for own tiles
+    if (S == 0) return mul_div(own, c, grid);
+    const long long total = own + S * R * cost, each = (S / groups + 1) * cost;
+    if (R <= grid && total > each * grid) {  // every CTA has room for own tiles
       long long prefix = S * R;  // prefix tiles of the CTAs before c
       if (c < grouped) {
         const int g = c / R;
-        prefix = group_start(g) * R + (group_start(g + 1) - group_start(g)) * (c - g * R);
+        const long long s = group_start(g);
+        prefix = s * R + (group_start(g + 1) - s) * (c - g * R);
       }
-      return total * c / grid - prefix;
+      return mul_div(total, c, grid) - prefix * cost;
     }
-    if (grouped < grid) return c <= grouped ? 0 : own * (c - grouped) / (grid - grouped);
-    return own * c / grid;
+    if (grouped < grid) return c <= grouped ? 0 : mul_div(own, c - grouped, grid - grouped);
+    return mul_div(own, c, grid);
   }
 };
 
-// A run of tiles of one block: tiles 0 .. n - 1 are keys key0 + 128 i up to kend.
+// A run of tiles of one block: keys key0 + 128 i, i < n, up to kend.
 struct Segment {
   const int32_t* list;  // pages
   int key0, kend, n;    // n = 0: no more segments
@@ -209,51 +242,60 @@ struct Segment {
   int slot;
 };
 
-constexpr int kSegRing = 8;
-constexpr int kSegReaders = kSoftWarps + kProdWarps + 1;
-
 struct Shared {
-  uint64_t full[10], empty[10];
-  uint64_t s_full[2], p_full[2], p_free[2], q_done[2], o_free[2], seg_full[kSegRing], seg_empty[kSegRing], drained;
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t s_full[2][2];                     // narrow, by softmax group and its tiles
+  uint64_t p_full[2], p_free[2];             // narrow, by tile
+  uint64_t ws_full[2], wp_full[2];           // wide, by group of rows
+  uint64_t q_done[2], o_full[2], o_free[2];  // by segment
+  uint64_t seg_full[kSegRing], seg_empty[kSegRing], drained;
   Segment seg[kSegRing];
   uint32_t tmem;
   int abort;
-  uint32_t live[8][kProdWarps];  // which keys of the tile exist, by tile number
-  float neg_ref[128], factor[128];
+  alignas(16) uint32_t live[8][4];  // which keys of a tile exist, by tile number
+  alignas(16) float neg_ref[2][kNarrow], factor[2][kNarrow];
   long long sum[16];
-  int found;
+  int found, found_len;
   long long found_start;
 };
+
+static_assert(sizeof(Shared) <= 2048, "beside the dynamic shared memory");
 
 // Bounded wait.  Once one has given up, the error is recorded, `abort` is set and
 // every later wait returns at once: the roles walk to their ends (within the same
 // bounds of memory) and the CTA leaves in the ordinary way.
 QE_DEV void wait_for(uint64_t* bar, uint32_t parity, Shared& sh, const AttnArgs& a) {
-  // the timer is read only once the first two tries (the second suspends the
-  // thread for up to 10 us) have failed
-  if (mbar_try_wait(bar, parity) || mbar_try_wait_sleep(bar, parity, 10000u)) return;
-  const uint64_t deadline = gtimer() + a.budget_ns;
-  while (!mbar_try_wait_sleep(bar, parity, 10000u)) {
+  uint64_t deadline = 0;
+  for (int i = 0; !mbar_try_wait(bar, parity); ++i) {
     if (*(volatile int*)&sh.abort) return;
-    if (gtimer() > deadline) {
+    if ((i & 15) != 15) continue;  // the timer is slow to read
+    const uint64_t now = gtimer();
+    if (deadline == 0) deadline = now + a.budget_ns;
+    if (now > deadline) {
       *(volatile int*)&sh.abort = 1;
       set_error(a.err, QE_ERR_TIMEOUT);
       return;
     }
   }
 }
+// The k-th completion (from 0) of a barrier that is one of two used in turn.  A wait
+// sees one bit of the phase: whoever waits for completion k has to know already that
+// k - 2 has happened (it waited for it, or for something that comes after it), and k + 2
+// must not happen before the wait is over.
+QE_DEV void wait_turn(uint64_t* pair, int k, Shared& sh, const AttnArgs& a) { wait_for(&pair[k & 1], (k >> 1) & 1, sh, a); }
 
-QE_DEV bool soft_vote(bool x) {  // over the softmax warps
+// The four softmax warps of a group.
+QE_DEV bool group_vote(int group, bool x) {
   uint32_t r;
   __syncwarp();
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r) : "r"((uint32_t)x) : "memory");
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r) : "r"((uint32_t)x), "r"(1 + group) : "memory");
   return r != 0;
 }
-QE_DEV void soft_sync() {
+QE_DEV void group_sync(int group) {
   __syncwarp();
-  asm volatile("bar.sync 1, 256;" ::: "memory");
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
 // ------------------------------------------------------------------- roles
@@ -278,7 +320,8 @@ struct Reader {
 
 // One thread: the CTA's segments in order, prefix first.
 template <int D>
-QE_DEV void deal_out(const AttnArgs& a, const Deal& d, long long t, long long t1, int b, long long b_start, int cap, Shared& sh) {
+QE_DEV void deal_out(const AttnArgs& a, const Deal& d, long long t, long long t1, int b, int len, long long b_start,
+                     int cap, Shared& sh) {
   constexpr int max_rows = Shape<D>::kRows;
   const int c = blockIdx.x, per = a.n_kv * a.rb_own;
   int at = 0;
@@ -304,7 +347,7 @@ QE_DEV void deal_out(const AttnArgs& a, const Deal& d, long long t, long long t1
       x.row0 = rb * max_rows;
       x.rows = min(max_rows, a.B * a.G - x.row0);
       long long s = s0;
-      x.h = (int)(s / a.prefix_tiles);
+      x.h = s < (1ll << 31) ? (int)((uint32_t)s / (uint32_t)a.prefix_tiles) : (int)(s / a.prefix_tiles);
       int i = (int)(s - (long long)x.h * a.prefix_tiles);
       while (s < s1) {
         x.n = (int)min((long long)(a.prefix_tiles - i), s1 - s);
@@ -322,38 +365,58 @@ QE_DEV void deal_out(const AttnArgs& a, const Deal& d, long long t, long long t1
     }
   }
   if (t < t1) {
-    int len = max(0, min(a.kv_len[b], cap)), nt = (len + kTile - 1) / kTile;
-    int unit = (int)((t - b_start) / nt), i = (int)(t - b_start - (long long)unit * nt);
+    int nt = (len + kTile - 1) / kTile, places = nt + kSegmentCost;
+    const long long in_row = t - b_start;
+    int unit = in_row < (1ll << 31) ? (int)((uint32_t)in_row / (uint32_t)places) : (int)(in_row / places);
+    int p = (int)(in_row - (long long)unit * places);
     for (;;) {
-      x.n = (int)min((long long)(nt - i), t1 - t);
-      x.h = unit / a.rb_own;
-      x.list = a.table + (size_t)b * a.table_stride;
-      x.key0 = i * kTile;
-      x.kend = len;
-      x.b = b;
-      x.row0 = (unit - x.h * a.rb_own) * max_rows;
-      x.rows = min(max_rows, a.G - x.row0);
-      const int u = b * per + unit;
-      x.slot = c + u;
-      if (i == 0) a.own_ctas[u].x = c;
-      if (i + x.n == nt) a.own_ctas[u].y = c;
-      put(x);
-      t += x.n;
+      const int p1 = (int)min((long long)places, p + (t1 - t));  // places [p, p1) of this block are this CTA's
+      const int i = max(0, p - kSegmentCost), i1 = max(0, p1 - kSegmentCost);
+      if (i < i1) {
+        const int u = b * per + unit;
+        x.n = i1 - i;
+        x.h = unit / a.rb_own;
+        x.list = a.table + (size_t)b * a.table_stride;
+        x.key0 = i * kTile;
+        x.kend = len;
+        x.b = b;
+        x.row0 = (unit - x.h * a.rb_own) * max_rows;
+        x.rows = min(max_rows, a.G - x.row0);
+        x.slot = c + u;
+        if (i == 0) a.own_ctas[u].x = c;
+        if (i1 == nt) a.own_ctas[u].y = c;
+        put(x);
+      }
+      t += p1 - p;
       if (t >= t1) break;
-      i = 0;
+      p = 0;
       if (++unit == per) {
         unit = 0;
         do {
           ++b;
           len = max(0, min(a.kv_len[b], cap));
         } while (len == 0 && b < a.B - 1);
-        nt = max(1, (len + kTile - 1) / kTile);
+        nt = (len + kTile - 1) / kTile;
+        places = nt + kSegmentCost;
       }
     }
   }
   x.n = 0;
   put(x);
 }
+
+// The order of the stages.  Tile g's K comes right before tile g - 1's V, so that its
+// scores can be computed while the softmax of g - 1 runs; only where narrow and wide
+// segments meet (and after the last tile) V comes first.  This counts, for the
+// consumer, the place of each K and V in that order.
+struct Places {
+  int k = 0, v = 0, next = 1;  // of the current K, of the V of the tile before it, and of what follows both
+  QE_DEV void step(bool v_first) {  // to the next tile
+    v = v_first ? next : next + 1;
+    k = v_first ? next + 1 : next;
+    next += 2;
+  }
+};
 
 template <typename T, int D>
 QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned char* qs) {
@@ -362,68 +425,15 @@ QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned
   constexpr int RPI = 32 / CH;        // rows a warp instruction copies
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftWarps;
   const int sub = lane % CH, sub_row = lane / CH;
-  // where this lane's piece of row 32 w + r goes, r = RPI i + sub_row: a swizzle of
-  // the row's low three bits, which are sub_row's and i's
   const uint32_t ring_u = smem_u32(ring) + (sub >> 3) * (kTile * 128) + (32 * w + sub_row) * 128;
   const uint32_t q_u = smem_u32(qs);
   int stage = 0, phase = 1;  // fresh empty barriers count as free
-  Reader reader;
-  Segment x;
-  int left = 0, key0 = 0, n = 0, seg = -1, rows_before = 0;
-  auto page_at = [&](int first) {
-    const int key = first + 32 * w + lane;
-    return key < x.kend ? __ldg(x.list + a.page.div((uint32_t)key)) : -1;
-  };
-  const T *k_row = nullptr, *v_row = nullptr, *v_next = nullptr;
+  unsigned long long k_row = 0, v_row = 0, v_next = 0;  // this lane's rows of the tile
   uint32_t live = 0, v_live = 0;
-  bool more = true;
-  while (true) {
-    // the next tile's keys
-    if (more && left == 0) {
-      reader.next(x, sh, a, true, lane == 0);
-      left = x.n;
-      key0 = x.key0;
-      more = left > 0;
-      if (more) {
-        // the block's queries, with its first tile's keys: two buffers for blocks of
-        // up to half the rows, the whole for larger ones
-        ++seg;
-        const bool wide = x.rows > Sh::kRows / 2 || rows_before > Sh::kRows / 2;
-        if (seg >= 2) wait_for(&sh.q_done[seg & 1], ((seg >> 1) - 1) & 1, sh, a);
-        if (seg >= 1 && wide) wait_for(&sh.q_done[(seg - 1) & 1], ((seg - 1) >> 1) & 1, sh, a);
-        __syncwarp();
-        rows_before = x.rows;
-        const int n16 = (x.rows + 15) & ~15;
-        const uint32_t dst = q_u + (x.rows <= Sh::kRows / 2 && (seg & 1) ? Sh::kRows / 2 * 128 : 0);
+  auto load = [&](bool is_v) {
 #pragma unroll 1
-        for (int e = threadIdx.x - 32 * kSoftWarps; e < n16 * (D / 8); e += 32 * kProdWarps) {
-          const int r = e / (D / 8), ch = e % (D / 8);
-          const T* src = (const T*)a.q;
-          if (r < x.rows) {
-            const int f = x.row0 + r;
-            src += x.b >= 0 ? (size_t)x.b * a.q_stride + (size_t)(x.h * a.G + f) * D
-                            : (size_t)(f / a.G) * a.q_stride + (size_t)(x.h * a.G + f % a.G) * D;
-          }
-          cp_async16z(dst + (ch >> 3) * (Sh::kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + ch * 8, r < x.rows);
-        }
-      }
-    }
-    if (more) {
-      const int key = key0 + 32 * w + lane, page = page_at(key0);
-      const bool ok = page >= 0 && page < a.n_pages;
-      if (key < x.kend && !ok) set_error(a.err, QE_ERR_INVALID_ARG);
-      live = __ballot_sync(0xffffffffu, ok);
-      const long long in_page = ((long long)x.h * a.page.d + (key - (int)a.page.div((uint32_t)key) * (int)a.page.d)) * D;
-      k_row = (const T*)a.kc + (ok ? page * a.k_page_stride + in_page : 0);
-      v_next = (const T*)a.vc + (ok ? page * a.v_page_stride + in_page : 0);
-      if (lane == 0) sh.live[n & 7][w] = live;
-    }
-    // K of this tile, then V of the one before
-#pragma unroll 1
-    for (int p = more ? 0 : Sh::kParts; p < (n > 0 ? 2 : 1) * Sh::kParts; ++p) {
-      const bool is_v = p >= Sh::kParts;
-      const unsigned long long row = (unsigned long long)(is_v ? v_row : k_row) +
-                                     2 * ((is_v ? p - Sh::kParts : p) * Sh::kDims);
+    for (int p = 0; p < Sh::kParts; ++p) {
+      const unsigned long long row = (is_v ? v_row : k_row) + 2 * p * Sh::kDims;
       const uint32_t lv = is_v ? v_live : live;
       wait_for(&sh.empty[stage], phase, sh, a);
       __syncwarp();
@@ -442,6 +452,66 @@ QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned
         phase ^= 1;
       }
     }
+  };
+  Reader reader;
+  Segment x;
+  int left = 0, key0 = 0, n = 0, seg = -1, rows_before = 0;
+  bool more = true;
+  while (true) {
+    bool first = false, v_first = false;
+    if (left == 0) {
+      reader.next(x, sh, a, true, lane == 0);
+      left = x.n;
+      key0 = x.key0;
+      more = left > 0;
+      first = more;
+      v_first = n > 0 && (!more || (x.rows > kNarrow) != (rows_before > kNarrow));
+    }
+    // at most two loads: (V, K) or (K, V); one of them at either end
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const bool is_v = (i == 0) == v_first;
+      if (is_v) {
+        if (n > 0) load(true);
+        continue;
+      }
+      if (!more) continue;
+      if (first) {
+        // the block's queries, with its first tile's keys: two narrow buffers, or one place for all
+        ++seg;
+        const bool wide = x.rows > kNarrow, whole = x.rows > Sh::kQLines / 2, whole_before = rows_before > Sh::kQLines / 2;
+        if (seg >= 2) wait_turn(sh.q_done, seg - 2, sh, a);
+        if (seg >= 1 && (whole || whole_before)) wait_turn(sh.q_done, seg - 1, sh, a);
+        if (seg >= 1 && wide && rows_before <= kNarrow) wait_turn(sh.o_full, seg - 1, sh, a);  // P is read no more
+        __syncwarp();
+        rows_before = x.rows;
+        const int fill = wide ? (x.rows + 127) & ~127 : (x.rows + 15) & ~15;
+        const uint32_t dst = q_u + (!whole && (seg & 1) ? Sh::kQLines / 2 * 128 : 0);
+#pragma unroll 1
+        for (int e = threadIdx.x - 32 * kSoftWarps; e < fill * (D / 8); e += 32 * kProdWarps) {
+          const int r = e / (D / 8), ch = e % (D / 8);
+          const T* src = (const T*)a.q;
+          if (r < x.rows) {
+            const int f = x.row0 + r, fb = a.group.div(f);
+            src += x.b >= 0 ? (size_t)x.b * a.q_stride + (size_t)(x.h * a.G + f) * D
+                            : (size_t)fb * a.q_stride + (size_t)(x.h * a.G + f - fb * a.G) * D;
+          }
+          const uint32_t line = wide ? (r >> 7) * (D * 256) + (ch >> 3) * (128 * 128) + (r & 127) * 128
+                                     : (ch >> 3) * (Sh::kQLines * 128) + r * 128;
+          cp_async16z(dst + line + (((ch & 7) ^ (r & 7)) << 4), src + ch * 8, r < x.rows);
+        }
+      }
+      const int key = key0 + 32 * w + lane;
+      const int page = key < x.kend ? __ldg(x.list + a.page.div((uint32_t)key)) : -1;
+      const bool ok = page >= 0 && page < a.n_pages;
+      if (key < x.kend && !ok) set_error(a.err, QE_ERR_INVALID_ARG);
+      live = __ballot_sync(0xffffffffu, ok);
+      const long long in_page = ((long long)x.h * a.page.d + (key - (int)a.page.div((uint32_t)key) * (int)a.page.d)) * D;
+      k_row = (unsigned long long)((const T*)a.kc + (ok ? page * a.k_page_stride + in_page : 0));
+      v_next = (unsigned long long)((const T*)a.vc + (ok ? page * a.v_page_stride + in_page : 0));
+      if (lane == 0) sh.live[n & 7][w] = live;
+      load(false);
+    }
     if (!more) break;
     v_row = v_next;
     v_live = live;
@@ -457,73 +527,141 @@ QE_DEV void multiply(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigne
                      uint32_t tmem) {
   using Sh = Shape<D>;
   const uint32_t ring_u = smem_u32(ring), q_u = smem_u32(qs), p_u = smem_u32(ps);
-  int stage = 0, phase = 0;
-  auto take = [&]() {
-    wait_for(&sh.full[stage], phase, sh, a);
+  // stage number `place * kParts + part` of the producers' order
+  auto take = [&](int at) {
+    wait_for(&sh.full[at % Sh::kStages], (at / Sh::kStages) & 1, sh, a);
     fence_async_smem();  // the copies wrote through the generic proxy, the products read through the async one
     tc_after();
-    return ring_u + stage * Sh::kStage;
+    return ring_u + at % Sh::kStages * Sh::kStage;
   };
-  auto give = [&]() {
-    mma_commit(&sh.empty[stage]);
-    if (++stage == Sh::kStages) {
-      stage = 0;
-      phase ^= 1;
+  auto give = [&](int at) { mma_commit(&sh.empty[at % Sh::kStages]); };
+  Places pl;
+  int n = 0;  // narrow tiles so far
+  int group_n[2] = {0, 0};  // of each softmax group
+  auto narrow_scores = [&](const Segment& x, int seg) {
+    const int n16 = (x.rows + 15) & ~15;
+    const uint32_t idesc = mma_idesc<T>(n16, false, false), d = tmem + (n & 1) * 128;
+    const uint32_t q_at = desc_low(q_u + (x.rows <= Sh::kQLines / 2 && (seg & 1) ? Sh::kQLines / 2 * 128 : 0), 16);
+#pragma unroll 1
+    for (int p = 0; p < Sh::kParts; ++p) {
+      const uint32_t k_at = desc_low(take(pl.k * Sh::kParts + p), 16), qp = q_at + p * (Sh::kDims / 64) * (Sh::kQLines * 128 / 16);
+#pragma unroll
+      for (int k = 0; k < Sh::kDims / 16; ++k)
+        mma_issue(d, k_at + (k >> 2) * (kTile * 128 / 16) + (k & 3) * 2, qp + (k >> 2) * (Sh::kQLines * 128 / 16) + (k & 3) * 2,
+                  idesc, p > 0 || k > 0);
+      give(pl.k * Sh::kParts + p);
+    }
+    mma_commit(&sh.s_full[seg & 1][group_n[seg & 1]++ & 1]);
+  };
+  auto narrow_outputs = [&](int m, int rows, int seg, bool first, int v_place) {
+    wait_turn(sh.p_full, m, sh, a);
+    const uint32_t idesc = mma_idesc<T>((rows + 15) & ~15, true, true), d = tmem + 256 + (seg & 1) * 128;
+    const uint32_t p_at = desc_low(p_u + (m & 1) * Sh::kP, kTile * 128);
+#pragma unroll 1
+    for (int p = 0; p < Sh::kParts; ++p) {
+      // head_dim 64: the second 64 dims repeat the first (leading offset 0); they are not read
+      const uint32_t v_at = desc_low(take(v_place * Sh::kParts + p), D == 64 ? 0 : kTile * 128);
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        mma_issue(d + p * 64, v_at + k * (2048 / 16), p_at + k * (2048 / 16), idesc, !first || k > 0);
+      give(v_place * Sh::kParts + p);
+    }
+    mma_commit(&sh.p_free[m & 1]);
+  };
+  auto wide_scores = [&](int blk, bool last_block) {
+    const uint32_t idesc = mma_idesc<T>(kTile, false, false), d = tmem + blk * 128;
+#pragma unroll 1
+    for (int p = 0; p < Sh::kParts; ++p) {
+      const uint32_t k_at = desc_low(take(pl.k * Sh::kParts + p), 16);
+      const uint32_t q_at = desc_low(q_u + blk * (D * 256) + p * (Sh::kDims / 64) * (128 * 128), 16);
+#pragma unroll
+      for (int k = 0; k < Sh::kDims / 16; ++k)
+        mma_issue(d, q_at + (k >> 2) * (128 * 128 / 16) + (k & 3) * 2, k_at + (k >> 2) * (kTile * 128 / 16) + (k & 3) * 2,
+                  idesc, p > 0 || k > 0);
+      if (last_block) give(pl.k * Sh::kParts + p);
+    }
+    mma_commit(&sh.ws_full[blk]);
+  };
+  auto wide_outputs = [&](int blk, bool last_block, bool first, int v_place) {
+    const uint32_t idesc = mma_idesc<T>(Sh::kDims, false, true), p_at = tmem + blk * 128;
+#pragma unroll 1
+    for (int p = 0; p < Sh::kParts; ++p) {
+      const uint32_t v_at = desc_low(take(v_place * Sh::kParts + p), kTile * 128), d = tmem + 256 + blk * 128 + p * 128;
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k) mma_issue_ta(d, p_at + k * 8, v_at + k * (2048 / 16), idesc, !first || k > 0);
+      if (last_block) give(v_place * Sh::kParts + p);
     }
   };
+
   Reader reader;
   Segment x;
-  int left = 0, seg = -1;               // of the scores
-  int o_n16 = 0, o_seg = 0;             // of the outputs, one tile behind
-  bool o_first = false, more = true;
-  for (int n = 0;; ++n) {
-    bool first = false;
-    if (more && left == 0) {
-      reader.next(x, sh, a, false, true);
-      left = x.n;
-      more = left > 0;
-      first = true;
-      ++seg;
-    }
-    const int n16 = (x.rows + 15) & ~15;
-    if (more) {
-      const uint32_t idesc = mma_idesc<T>(n16, false);
-      const uint32_t q_at = desc_low(q_u + (x.rows <= Sh::kRows / 2 && (seg & 1) ? Sh::kRows / 2 * 128 : 0), 16);
-      const uint32_t d = tmem + (n & 1) * 128;
-#pragma unroll 1
-      for (int p = 0; p < Sh::kParts; ++p) {
-        const uint32_t k_at = desc_low(take(), 16), qp = q_at + p * (Sh::kDims / 64) * (Sh::kRows * 128 / 16);
-#pragma unroll
-        for (int k = 0; k < Sh::kDims / 16; ++k)
-          mma_issue(d, k_at + (k >> 2) * (kTile * 128 / 16) + (k & 3) * 2, qp + (k >> 2) * (Sh::kRows * 128 / 16) + (k & 3) * 2,
-                    idesc, p > 0 || k > 0);
-        give();
+  reader.next(x, sh, a, false, true);
+  bool wide_before = false;
+  int wide_n = 0;  // wide tiles so far, by which the phases of wp_full go (block 1 may have had fewer)
+  int wide_n1 = 0;
+  // the narrow tile whose outputs are still to be issued
+  bool pending = false, pend_first = false;
+  int pend_rows = 0, pend_seg = 0;
+  for (int seg = 0; x.n > 0; ++seg) {
+    const bool wide = x.rows > kNarrow;
+    Segment y;
+    if (!wide) {
+      for (int i = 0; i < x.n; ++i) {
+        // (the place of this tile's K was set when the tile before it was left)
+        narrow_scores(x, seg);
+        if (i == x.n - 1) mma_commit(&sh.q_done[seg & 1]);
+        if (pending) {
+          narrow_outputs(n - 1, pend_rows, pend_seg, pend_first, pl.v);
+          if (pend_seg != seg) mma_commit(&sh.o_full[pend_seg & 1]);
+        }
+        pending = true;
+        pend_rows = x.rows;
+        pend_seg = seg;
+        pend_first = i == 0;
+        ++n;
+        if (i == 0) {  // before the first outputs of this segment
+          if (seg >= 2) wait_turn(sh.o_free, seg - 2, sh, a);
+          if (wide_before) wait_turn(sh.o_free, seg - 1, sh, a);
+        }
+        bool v_first = false;
+        if (i == x.n - 1) {
+          reader.next(y, sh, a, false, true);
+          v_first = y.n == 0 || y.rows > kNarrow;
+        }
+        pl.step(v_first);
+        if (v_first) {
+          narrow_outputs(n - 1, pend_rows, pend_seg, pend_first, pl.v);
+          mma_commit(&sh.o_full[seg & 1]);
+          pending = false;
+        }
       }
-      mma_commit(&sh.s_full[n & 1]);
-      if (--left == 0) mma_commit(&sh.q_done[seg & 1]);
-    }
-    if (n > 0) {  // the outputs of tile n - 1
-      const int m = n - 1;
-      if (o_first && o_seg >= 2) wait_for(&sh.o_free[o_seg & 1], ((o_seg >> 1) - 1) & 1, sh, a);
-      wait_for(&sh.p_full[m & 1], (m >> 1) & 1, sh, a);
-      const uint32_t idesc = mma_idesc<T>(o_n16, true);
-      const uint32_t d = tmem + 256 + (o_seg & 1) * 128;
-      const uint32_t p_at = desc_low(p_u + (o_n16 <= 64 && (m & 1) ? Sh::kP / 2 : 0), kTile * 128);
-#pragma unroll 1
-      for (int p = 0; p < Sh::kParts; ++p) {
-        // head_dim 64: the second 64 dims repeat the first (leading offset 0); they are not read
-        const uint32_t v_at = desc_low(take(), D == 64 ? 0 : kTile * 128);
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_issue(d + p * 64, v_at + k * (2048 / 16), p_at + k * (2048 / 16), idesc, !o_first || k > 0);
-        give();
+    } else {
+      const int blocks = (x.rows + 127) >> 7;
+      if (seg >= 2) wait_turn(sh.o_free, seg - 2, sh, a);
+      if (seg >= 1) wait_turn(sh.o_free, seg - 1, sh, a);
+      for (int blk = 0; blk < blocks; ++blk) wide_scores(blk, blk == blocks - 1);
+      if (x.n == 1) mma_commit(&sh.q_done[seg & 1]);
+      for (int i = 0; i < x.n; ++i) {
+        bool v_first = false;
+        if (i == x.n - 1) {
+          reader.next(y, sh, a, false, true);
+          v_first = y.n == 0 || y.rows <= kNarrow;
+        }
+        pl.step(v_first);
+        for (int blk = 0; blk < blocks; ++blk) {
+          wait_for(&sh.wp_full[blk], (blk ? wide_n1 : wide_n) & 1, sh, a);
+          tc_after();
+          wide_outputs(blk, blk == blocks - 1, i == 0, pl.v);
+          if (i + 1 < x.n) wide_scores(blk, blk == blocks - 1);
+        }
+        ++wide_n;
+        wide_n1 += blocks - 1;
+        if (i + 2 == x.n) mma_commit(&sh.q_done[seg & 1]);
       }
-      mma_commit(&sh.p_free[m & 1]);
+      mma_commit(&sh.o_full[seg & 1]);
     }
-    if (!more) break;
-    o_n16 = n16;
-    o_seg = seg;
-    o_first = first;
+    wide_before = wide;
+    x = y;
   }
   // whatever happened, nothing is in flight when this returns
   mma_commit(&sh.drained);
@@ -535,56 +673,102 @@ QE_DEV void multiply(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigne
     }
 }
 
+// One narrow segment, by the group whose turn it is: a thread has one key (lane of
+// S^T) and all columns.  n: number of its first tile among the narrow ones; own_n:
+// among the group's; tile: among all.  The scores of tile n are issued after the
+// outputs of tile n - 2, so that once they are there, that P has been read.
 template <typename T, int D>
-QE_DEV void soften(const AttnArgs& a, Shared& sh, unsigned char* ps, uint32_t tmem_base) {
+QE_DEV void soften_narrow(const AttnArgs& a, const Segment& x, int seg, int n, int own_n, int tile, Shared& sh,
+                          unsigned char* ps, uint32_t tmem_base) {
   using Sh = Shape<D>;
-  constexpr int J = Sh::kRows / 32;  // most batches of 16 columns a thread has
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, side = threadIdx.x >> 7;
-  const int key = 32 * w + lane;
-  const uint32_t tmem = tmem_base + ((uint32_t)(32 * w) << 16);
+  constexpr int J = kNarrow / 16;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7, key = threadIdx.x & 127;
+  const uint32_t tmem = tmem_base + ((uint32_t)(32 * w) << 16), o_at = tmem + 256 + (seg & 1) * 128;
+  const int nb = (x.rows + 15) >> 4;
   float l[J][16];
 #pragma unroll
   for (int j = 0; j < J; ++j)
 #pragma unroll
     for (int e = 0; e < 16; ++e) l[j][e] = 0.f;
-  int seg = -1, left = 0;
-  bool wide = false, wide_before = false;  // more than 64 rows: P takes both buffers
-  Reader reader;
-  Segment x;
-  for (int n = 0;; ++n) {
-    bool first = false;
-    if (left == 0) {
-      reader.next(x, sh, a, true, lane == 0);
-      // the warps have to go through the same barriers: they end together
-      if (soft_vote(x.n == 0)) break;
-      left = x.n;
-      first = true;
-      ++seg;
-    }
-    const int nb = (x.rows + 15) >> 4;
-    wide_before = wide;
-    wide = nb > 4;
-    const uint32_t s_at = tmem + (n & 1) * 128, o_at = tmem + 256 + (seg & 1) * 128;
-    wait_for(&sh.s_full[n & 1], (n >> 1) & 1, sh, a);
+  float* ref = sh.neg_ref[group];
+  float* factor = sh.factor[group];
+#pragma unroll 1
+  for (int i = 0; i < x.n; ++i, ++n, ++own_n, ++tile) {
+    const uint32_t s_at = tmem + (n & 1) * 128;
+    wait_turn(sh.s_full[group], own_n, sh, a);
     __syncwarp();
     tc_after();
-    const bool live = (sh.live[n & 7][w] >> lane) & 1;
+    const bool live = (sh.live[tile & 7][w] >> lane) & 1;
     float p[J][16];
 #pragma unroll 1
-    for (int pass = 0;; ++pass) {
+    for (bool raise = i == 0;; raise = true) {
+      if (raise) {
+        // raise the references to the maxima so far; no product reads this P or writes o meanwhile
+        if (i > 0) wait_turn(sh.p_free, n - 1, sh, a);
+        __syncwarp();
+        tc_after();
+        float* scratch = reinterpret_cast<float*>(ps + (n & 1) * Sh::kP);
+#pragma unroll 1
+        for (int bb = 0; bb < nb; ++bb) {
+          float v[16];
+          __syncwarp();
+          tmem_ld16(s_at + bb * 16, v);
+          tmem_wait_ld(v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = live ? v[e] * a.scale_log2 : -INFINITY;
+          const float m = warp_reduce_rows_max<16>(v, lane);
+          if ((lane & 1) == 0) scratch[w * kNarrow + bb * 16 + reduced_row_of_lane<16>(lane)] = m;
+        }
+        group_sync(group);
+        if (key < nb * 16) {
+          const float old = i == 0 ? -kNoRef : -ref[key];
+          const float m = fmaxf(fmaxf(fmaxf(scratch[key], scratch[kNarrow + key]),
+                                      fmaxf(scratch[2 * kNarrow + key], scratch[3 * kNarrow + key])), old);
+          ref[key] = -m;
+          factor[key] = exp2_approx(old - m);
+        }
+        group_sync(group);
+        if (i > 0) {
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+            if (j < nb) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const float4 r = *reinterpret_cast<const float4*>(factor + j * 16 + e);
+                l[j][e] *= r.x;
+                l[j][e + 1] *= r.y;
+                l[j][e + 2] *= r.z;
+                l[j][e + 3] *= r.w;
+              }
+            }
+#pragma unroll 1
+          for (int c = 0; c < nb * Sh::kParts; ++c) {
+            const int bb = c % nb, d = c / nb;
+            float o[16];
+            const uint32_t at = o_at + d * 64 + bb * 16;
+            __syncwarp();
+            tmem_ld16(at, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] *= factor[bb * 16 + e];
+            tmem_st16(at, o);
+          }
+          tmem_wait_st();
+        }
+        __syncwarp();
+      }
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (2 * j + side < nb) tmem_ld16(s_at + (2 * j + side) * 16, p[j]);
+        if (j < nb) tmem_ld16(s_at + j * 16, p[j]);
 #pragma unroll
       for (int j = 0; j < J; ++j) tmem_wait_ld(p[j]);
       float most = -INFINITY;
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (2 * j + side < nb) {
-          const float4* ref = reinterpret_cast<const float4*>(sh.neg_ref + (2 * j + side) * 16);
+        if (j < nb) {
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
-            const float4 r = ref[e / 4];
+            const float4 r = *reinterpret_cast<const float4*>(ref + j * 16 + e);
             p[j][e] = fmaf(p[j][e], a.scale_log2, r.x);
             p[j][e + 1] = fmaf(p[j][e + 1], a.scale_log2, r.y);
             p[j][e + 2] = fmaf(p[j][e + 2], a.scale_log2, r.z);
@@ -599,77 +783,16 @@ QE_DEV void soften(const AttnArgs& a, Shared& sh, unsigned char* ps, uint32_t tm
           }
           most = fmaxf(most, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
         }
-      if (pass > 0 || !soft_vote(most > kSlack)) break;
-      // raise the references to the maxima so far; no product reads ps or writes o meanwhile
-      if (n > 1) wait_for(&sh.p_free[n & 1], ((n >> 1) - 1) & 1, sh, a);
-      if (n > 0) wait_for(&sh.p_free[(n - 1) & 1], ((n - 1) >> 1) & 1, sh, a);
-      __syncwarp();
-      tc_after();
-      float* scratch = reinterpret_cast<float*>(ps);
-#pragma unroll 1
-      for (int bb = side; bb < nb; bb += 2) {
-        float v[16];
-        __syncwarp();
-        tmem_ld16(s_at + bb * 16, v);
-        tmem_wait_ld(v);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = live ? v[e] * a.scale_log2 : -INFINITY;
-        const float m = warp_reduce_rows_max<16>(v, lane);
-        if ((lane & 1) == 0) scratch[w * 128 + bb * 16 + reduced_row_of_lane<16>(lane)] = m;
-      }
-      soft_sync();
-      if (threadIdx.x < nb * 16) {
-        const int col = threadIdx.x;
-        const float old = -sh.neg_ref[col];
-        const float m = fmaxf(fmaxf(fmaxf(scratch[col], scratch[128 + col]), fmaxf(scratch[256 + col], scratch[384 + col])), old);
-        sh.neg_ref[col] = -m;
-        sh.factor[col] = exp2_approx(old - m);
-      }
-      soft_sync();
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (2 * j + side < nb) {
-          const float4* f = reinterpret_cast<const float4*>(sh.factor + (2 * j + side) * 16);
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float4 r = f[e / 4];
-            l[j][e] *= r.x;
-            l[j][e + 1] *= r.y;
-            l[j][e + 2] *= r.z;
-            l[j][e + 3] *= r.w;
-          }
-        }
-      if (!first) {
-#pragma unroll 1
-        for (int i = side; i < nb * Sh::kParts; i += 2) {
-          const int bb = i % nb, d = i / nb;
-          float o[16];
-          const uint32_t at = o_at + d * 64 + bb * 16;
-          __syncwarp();
-          tmem_ld16(at, o);
-          tmem_wait_ld(o);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] *= sh.factor[bb * 16 + e];
-          tmem_st16(at, o);
-        }
-        tmem_wait_st();
-      }
-      __syncwarp();
+      if (raise || !group_vote(group, most > kSlack)) break;
     }
-    // the P that was in this place has been read
-    if (n > 1) wait_for(&sh.p_free[n & 1], ((n >> 1) - 1) & 1, sh, a);
-    if (n > 0 && (wide || wide_before)) wait_for(&sh.p_free[(n - 1) & 1], ((n - 1) >> 1) & 1, sh, a);
-    __syncwarp();
-    unsigned char* p_row = ps + (!wide && (n & 1) ? Sh::kP / 2 : 0) + key * Sh::kPRow;
+    unsigned char* p_row = ps + (n & 1) * Sh::kP + key * 128;
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      if (2 * j + side < nb) {
-        const int bb = 2 * j + side;
-        const int c = (bb & 3) * 2;
+      if (j < nb) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const float* v = p[j] + 8 * hf;
-          *reinterpret_cast<uint4*>(p_row + (bb >> 2) * (kTile * 128) + (((c + hf) ^ (key & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(p_row + (((2 * j + hf) ^ (key & 7)) << 4)) =
               make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
         }
 #pragma unroll
@@ -679,49 +802,195 @@ QE_DEV void soften(const AttnArgs& a, Shared& sh, unsigned char* ps, uint32_t tm
     tc_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.p_full[n & 1]);
-    if (--left > 0) continue;
+  }
+  // the segment's results: each warp leaves its part of l
+  const size_t row_at = x.b >= 0 ? (size_t)x.slot * a.own_rows : (size_t)x.slot * a.B * a.G + x.row0;
+  float* po = (x.b >= 0 ? a.part_own : a.part_prefix) + row_at * D + key;
+  float2* pml = (x.b >= 0 ? a.ml_own : a.ml_prefix) + row_at * 4 + w;
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+    if (j < nb) {
+      const float sum = warp_reduce_rows<16>(l[j], lane);
+      const int col = j * 16 + reduced_row_of_lane<16>(lane);
+      if ((lane & 1) == 0 && col < x.rows) pml[col * 4] = make_float2(-ref[col], sum);
+    }
+  wait_turn(sh.o_full, seg, sh, a);
+  __syncwarp();
+  tc_after();
+#pragma unroll 1
+  for (int c = 0; c < nb * Sh::kParts; ++c) {
+    const int bb = c % nb, d = c / nb;
+    float o[16];
+    __syncwarp();
+    tmem_ld16(o_at + d * 64 + bb * 16, o);
+    tmem_wait_ld(o);
+    if (D >= 128 || key < D) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (bb * 16 + e < x.rows) po[(size_t)(bb * 16 + e) * D + d * 128] = o[e];
+    }
+  }
+  tc_before();
+  __syncwarp();
+  if (lane < 2) mbar_arrive(&sh.o_free[seg & 1]);  // for the other group's four warps too
+}
 
-    // the segment's results
-    if (n > 0) wait_for(&sh.p_free[(n - 1) & 1], ((n - 1) >> 1) & 1, sh, a);
-    wait_for(&sh.p_free[n & 1], (n >> 1) & 1, sh, a);
+// One wide segment, one group's 128 rows: a thread has one row.  n: number of the
+// first tile among the group's wide ones.
+template <typename T, int D>
+QE_DEV void soften_wide(const AttnArgs& a, const Segment& x, int seg, int n, int tile, Shared& sh, uint32_t tmem_base) {
+  using Sh = Shape<D>;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
+  const uint32_t tmem = tmem_base + ((uint32_t)(32 * w) << 16), s_at = tmem + group * 128, o_at = tmem + 256 + group * 128;
+  const int row = threadIdx.x;  // of the block: group * 128 + lane of the accumulator
+  float neg = kNoRef, l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < x.n; ++i, ++n, ++tile) {
+    wait_for(&sh.ws_full[group], n & 1, sh, a);  // the outputs of the tile before are complete then, too
     __syncwarp();
     tc_after();
-    float* scratch = reinterpret_cast<float*>(ps);
-    const size_t row_at = x.b >= 0 ? (size_t)x.slot * a.own_rows : (size_t)x.slot * a.B * a.G + x.row0;
-    float* po = (x.b >= 0 ? a.part_own : a.part_prefix) + row_at * D + key;
-    float2* pml = (x.b >= 0 ? a.ml_own : a.ml_prefix) + row_at;
+    const uint4 live = *reinterpret_cast<const uint4*>(sh.live[tile & 7]);
+    const uint32_t words[4] = {live.x, live.y, live.z, live.w};
+    const bool all = (live.x & live.y & live.z & live.w) == 0xffffffffu;
+    float top = -INFINITY;
 #pragma unroll 1
-    for (int i = side; i < nb * Sh::kParts; i += 2) {
-      const int bb = i % nb, d = i / nb;
-      float o[16];
+    for (int c = 0; c < 4; ++c) {
+      float v[16], u[16];
       __syncwarp();
-      tmem_ld16(o_at + d * 64 + bb * 16, o);
-      tmem_wait_ld(o);
-      if (D >= 128 || key < D) {
+      tmem_ld16(s_at + c * 32, v);
+      tmem_ld16(s_at + c * 32 + 16, u);
+      tmem_wait_ld(v);
+      tmem_wait_ld(u);
+      if (!all) {
+        const uint32_t m = c == 0 ? words[0] : c == 1 ? words[1] : c == 2 ? words[2] : words[3];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (bb * 16 + e < x.rows) po[(size_t)(bb * 16 + e) * D + d * 128] = o[e];
+        for (int e = 0; e < 16; ++e) {
+          if (!((m >> e) & 1)) v[e] = -INFINITY;
+          if (!((m >> (e + 16)) & 1)) u[e] = -INFINITY;
+        }
+      }
+      float t0 = fmaxf(v[0], u[0]), t1 = fmaxf(v[1], u[1]);
+#pragma unroll
+      for (int e = 2; e < 16; e += 2) {
+        t0 = fmaxf(t0, fmaxf(v[e], u[e]));
+        t1 = fmaxf(t1, fmaxf(v[e + 1], u[e + 1]));
+      }
+      top = fmaxf(top, fmaxf(t0, t1));
+    }
+    top *= a.scale_log2;  // scale >= 0; 0 times an infinity gives NaN, which raises nothing
+    const bool raise = top + neg > kSlack;
+    if (__any_sync(0xffffffffu, raise)) {
+      float f = 1.f;
+      if (raise) {
+        f = exp2_approx(-neg - top);
+        neg = -top;
+      }
+      l0 *= f;
+      l1 *= f;
+      l2 *= f;
+      l3 *= f;
+      if (i > 0) {
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          float o[16];
+          __syncwarp();
+          tmem_ld16(o_at + c * 16, o);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] *= f;
+          tmem_st16(o_at + c * 16, o);
+        }
       }
     }
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      float v[16], u[16];
+      uint32_t pk[16];
+      __syncwarp();
+      tmem_ld16(s_at + c * 32, v);
+      tmem_ld16(s_at + c * 32 + 16, u);
+      tmem_wait_ld(v);
+      tmem_wait_ld(u);
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (2 * j + side < nb) {
-        const float sum = warp_reduce_rows<16>(l[j], lane);
-        if ((lane & 1) == 0) scratch[w * 128 + (2 * j + side) * 16 + reduced_row_of_lane<16>(lane)] = sum;
+      for (int e = 0; e < 16; ++e) {
+        v[e] = exp2_approx(fmaf(v[e], a.scale_log2, neg));
+        u[e] = exp2_approx(fmaf(u[e], a.scale_log2, neg));
       }
+      if (!all) {
+        const uint32_t m = c == 0 ? words[0] : c == 1 ? words[1] : c == 2 ? words[2] : words[3];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (!((m >> e) & 1)) v[e] = 0.f;
+          if (!((m >> (e + 16)) & 1)) u[e] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        l0 += v[e];
+        l1 += v[e + 1];
+        l2 += u[e];
+        l3 += u[e + 1];
+        pk[e / 2] = pack2<T>(v[e], v[e + 1]);
+        pk[8 + e / 2] = pack2<T>(u[e], u[e + 1]);
+      }
+      tmem_st16(s_at + c * 16, pk);  // over scores that have been read
+    }
+    tmem_wait_st();
     tc_before();
-    soft_sync();
-    if (threadIdx.x < x.rows) {
-      const int col = threadIdx.x;
-      pml[col] = make_float2(-sh.neg_ref[col], (scratch[col] + scratch[128 + col]) + (scratch[256 + col] + scratch[384 + col]));
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.wp_full[group]);
+  }
+  wait_turn(sh.o_full, seg, sh, a);
+  __syncwarp();
+  tc_after();
+  const size_t row_at = x.b >= 0 ? (size_t)x.slot * a.own_rows : (size_t)x.slot * a.B * a.G + x.row0;
+  float* po = (x.b >= 0 ? a.part_own : a.part_prefix) + (row_at + row) * D;
+#pragma unroll 1
+  for (int c = 0; c < D / 16; ++c) {
+    float o[16];
+    __syncwarp();
+    tmem_ld16(o_at + c * 16, o);
+    tmem_wait_ld(o);
+    if (row < x.rows) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<float4*>(po + c * 16 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
     }
-    if (threadIdx.x < 128) sh.neg_ref[threadIdx.x] = kNoRef;
-    soft_sync();
-    if (lane == 0) mbar_arrive(&sh.o_free[seg & 1]);
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) l[j][e] = 0.f;
+  }
+  if (row < x.rows) {
+    float4* pml = reinterpret_cast<float4*>((x.b >= 0 ? a.ml_own : a.ml_prefix) + (row_at + row) * 4);
+    pml[0] = make_float4(-neg, l0, -neg, l1);
+    pml[1] = make_float4(-neg, l2, -neg, l3);
+  }
+  tc_before();
+}
+
+template <typename T, int D>
+QE_DEV void soften(const AttnArgs& a, Shared& sh, unsigned char* ps, uint32_t tmem) {
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 7;
+  Reader reader;
+  Segment x;
+  int n = 0, own_n = 0, wide_n = 0, tile = 0;
+#pragma unroll 1
+  for (int seg = 0;; ++seg) {
+    reader.next(x, sh, a, true, lane == 0);
+    // a group's warps have to go through the same barriers: they end together
+    if (group_vote(group, x.n == 0)) break;
+    if (x.rows > kNarrow) {
+      if (group * 128 < x.rows) {
+        soften_wide<T, D>(a, x, seg, wide_n, tile, sh, tmem);
+        wide_n += x.n;
+        __syncwarp();
+        if (lane < (x.rows > 128 ? 1 : 2)) mbar_arrive(&sh.o_free[seg & 1]);  // 2: for the group without rows, too
+      }
+    } else {
+      if ((seg & 1) == group) {
+        soften_narrow<T, D>(a, x, seg, n, own_n, tile, sh, ps, tmem);
+        own_n += x.n;
+      }
+      n += x.n;
+    }
+    tile += x.n;
   }
 }
 
@@ -740,10 +1009,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) qe_attn_part_kernel(const __g
       mbar_init(&sh.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], kSoftWarps);
+      mbar_init(&sh.s_full[0][i], 1);
+      mbar_init(&sh.s_full[1][i], 1);
+      mbar_init(&sh.p_full[i], kSoftWarps / 2);
       mbar_init(&sh.p_free[i], 1);
+      mbar_init(&sh.ws_full[i], 1);
+      mbar_init(&sh.wp_full[i], kSoftWarps / 2);
       mbar_init(&sh.q_done[i], 1);
+      mbar_init(&sh.o_full[i], 1);
       mbar_init(&sh.o_free[i], kSoftWarps);
     }
     for (int i = 0; i < kSegRing; ++i) {
@@ -754,16 +1027,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1) qe_attn_part_kernel(const __g
     fence_mbar_init();
     sh.abort = 0;
   }
-  if (threadIdx.x < 128) sh.neg_ref[threadIdx.x] = kNoRef;
+  if (warp == 12) {
+    __syncwarp();
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    tc_before();
+  }
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // the total of own tiles, then the batch row in which this CTA's share starts
+  // where this CTA's share of the own line starts: one pass over the lengths for
+  // up to 512 rows, a sum and a search for more
   const int cap = (int)min((long long)a.table_stride * a.page.d, 1ll << 30);
   const int per = a.n_kv * a.rb_own;
-  auto tiles_of = [&](int b) { return b < a.B ? (max(0, min(a.kv_len[b], cap)) + kTile - 1) / kTile : 0; };
-  // inclusive sums over the CTA's threads; the total in sh.sum[16]
-  auto block_scan = [&](long long v) {
+  auto len_of = [&](int b) {
+    if (b >= a.B) return 0;
+    const int n = a.kv_len[b];
+    if (n > cap && blockIdx.x == 0) set_error(a.err, QE_ERR_INVALID_ARG);
+    return max(0, min(n, cap));
+  };
+  auto places_of = [&](int len) { return len > 0 ? (len + kTile - 1) / kTile + kSegmentCost : 0; };
+  auto block_scan = [&](long long v) {  // {inclusive sum, total} over the CTA
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const long long u = __shfl_up_sync(0xffffffffu, v, d);
@@ -773,61 +1057,59 @@ __global__ void __launch_bounds__(kAttnThreads, 1) qe_attn_part_kernel(const __g
     if (lane == 31) sh.sum[warp] = v;
     __syncthreads();
     long long all = 0;
-#pragma unroll 1
+#pragma unroll
     for (int i = 0; i < kAttnThreads / 32; ++i) {
-      if (i == warp) v += all;
-      all += sh.sum[i];
+      const long long s = sh.sum[i];
+      if (i < warp) v += s;
+      all += s;
     }
     return make_longlong2(v, all);
   };
-  long long mine = 0;
-  for (int b = threadIdx.x; b < a.B; b += kAttnThreads) {
-    mine += tiles_of(b);
-    if (blockIdx.x == 0 && a.kv_len[b] > cap) set_error(a.err, QE_ERR_INVALID_ARG);
-  }
-  const longlong2 sums = block_scan(mine);
-  const Deal deal(a, sums.y * per);
+  int len = len_of(threadIdx.x);
+  long long mine = places_of(len);
+  for (int b = threadIdx.x + kAttnThreads; b < a.B; b += kAttnThreads) mine += places_of(len_of(b));
+  longlong2 scan = block_scan(mine);
+  const Deal deal(a, scan.y * per);
   const long long t0 = deal.own_start(blockIdx.x), t1 = deal.own_start(blockIdx.x + 1);
   if (threadIdx.x == 0) {
     a.own_start[blockIdx.x] = t0;
     if (blockIdx.x == gridDim.x - 1) a.own_start[gridDim.x] = deal.own;
   }
-  if (t0 == t1 && blockIdx.x >= deal.grouped) return;  // uniform over the CTA
-  if (warp == 12) {
-    __syncwarp();
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    tc_before();
-  }
   if (t0 < t1) {
-    long long before = 0;  // tiles of the rows of earlier passes, per key head and row block
+    long long before = 0;  // places of the rows of earlier passes, per key head and row block
     for (int b0 = 0; b0 < a.B && before * per <= t0; b0 += kAttnThreads) {
-      const int b = b0 + threadIdx.x, nt = tiles_of(b);
-      const longlong2 scan = block_scan(nt);
-      const long long end = (before + scan.x) * per, start = end - (long long)nt * per;
+      if (a.B > kAttnThreads) {
+        len = len_of(b0 + threadIdx.x);
+        scan = block_scan(places_of(len));
+      }
+      const long long end = (before + scan.x) * per, start = end - (long long)places_of(len) * per;
       if (start <= t0 && t0 < end) {
-        sh.found = b;
+        sh.found = b0 + threadIdx.x;
+        sh.found_len = len;
         sh.found_start = start;
       }
       before += scan.y;
     }
   }
+  tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = *(volatile uint32_t*)&sh.tmem;
-  if (warp < kSoftWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    soften<T, D>(a, sh, ps, tmem);
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp < kSoftWarps + kProdWarps) {
-      produce<T, D>(a, sh, ring, qs);
-    } else if (warp == 12) {
-      if (lane == 0) multiply<T, D>(a, sh, ring, qs, ps, tmem);
-      __syncwarp();
-    } else if (warp == 13) {
-      if (lane == 0) deal_out<D>(a, deal, t0, t1, sh.found, sh.found_start, cap, sh);
-      __syncwarp();
+  if (t0 < t1 || blockIdx.x < deal.grouped) {  // uniform over the CTA
+    if (warp < kSoftWarps) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+      soften<T, D>(a, sh, ps, tmem);
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+      if (warp < kSoftWarps + kProdWarps) {
+        produce<T, D>(a, sh, ring, qs);
+      } else if (warp == 12) {
+        if (lane == 0) multiply<T, D>(a, sh, ring, qs, ps, tmem);
+        __syncwarp();
+      } else if (warp == 13) {
+        if (lane == 0) deal_out<D>(a, deal, t0, t1, sh.found, sh.found_len, sh.found_start, cap, sh);
+        __syncwarp();
+      }
     }
   }
   tc_before();
@@ -870,13 +1152,13 @@ __global__ void __launch_bounds__(128) qe_attn_join_kernel(const __grid_constant
     size_t at;
     if (i < np) {
       at = (size_t)(g0 + i + h) * a.B * a.G + (size_t)b * a.G + g;
-      *ml = a.ml_prefix + at;
+      *ml = a.ml_prefix + at * 4;
       *o = a.part_prefix + at * D;
       return true;
     }
     const int c = c0 + i - np;
     at = (size_t)(c + unit) * a.own_rows + g % max_rows;
-    *ml = a.ml_own + at;
+    *ml = a.ml_own + at * 4;
     *o = a.part_own + at * D;
     return a.own_start[c] < a.own_start[c + 1];
   };
@@ -895,7 +1177,10 @@ __global__ void __launch_bounds__(128) qe_attn_join_kernel(const __grid_constant
     if (i < np + no) {
       const float2* p;
       has = where(i, &p, &o);
-      if (has) ml = *p;
+      if (has) {
+        const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 2);
+        ml = make_float2(u.x, (u.y + u.w) + (v.y + v.w));
+      }
     }
     const float top = fmaxf(m, warp_max(ml.x)), f0 = exp2_approx(m - top), f = has ? exp2_approx(ml.x - top) : 0.f;
     m = top;
@@ -975,8 +1260,8 @@ AttnPlan attn_plan(int n_kv, int n_q, int D, int B, int sms) {
   p.off_cta = take(8 * ((size_t)p.grid + 1));
   p.off_own = take(sizeof(int2) * (size_t)B * n_kv * p.rb_own);
   p.off_groups = take(sizeof(int2) * (size_t)n_kv);
-  p.off_mlp = take(sizeof(float2) * rows_p);
-  p.off_mlo = take(sizeof(float2) * rows_o);
+  p.off_mlp = take(4 * sizeof(float2) * rows_p);
+  p.off_mlo = take(4 * sizeof(float2) * rows_o);
   p.off_pp = take(4 * rows_p * D);
   p.off_po = take(4 * rows_o * D);
   p.total = off;
@@ -1055,6 +1340,7 @@ extern "C" QE_API int attn_decode_step(const qe_kv_cache* c, int B, int n_q, con
   if (prefix_len < 0 || prefix_len >= 1 << 30) return fail(QE_ERR_INVALID_ARG, "prefix_len must be in [0, 2^30) (got %d)", prefix_len);
   if (table_stride < 0 || (int64_t)table_stride * c->page_size >= 1ll << 30)
     return fail(QE_ERR_INVALID_ARG, "table_stride * page_size must be in [0, 2^30)");
+  if (!(scale >= 0.f && scale <= 3.0e38f)) return fail(QE_ERR_INVALID_ARG, "scale must be finite and >= 0 (got %g)", scale);
   if (B == 0) return QE_OK;
   const int D = c->head_dim;
   if ((rc = check_ptr(q, "q", false, 16)) || (rc = check_ptr(out, "out", false, 16)) || (rc = check_ptr(kv_len, "kv_len")) ||
@@ -1092,6 +1378,9 @@ extern "C" QE_API int attn_decode_step(const qe_kv_cache* c, int B, int n_q, con
   a.rb_prefix = p.rb_prefix; a.rb_own = p.rb_own; a.own_rows = p.own_rows;
   a.scale_log2 = scale * kLog2e;
   a.page = fast_div((uint32_t)c->page_size);
+  a.group = fast_div((uint32_t)a.G);
+  // a wide tile of two blocks of 128 rows takes about twice a narrow one's time
+  a.prefix_cost = (long long)B * a.G > 128 && p.max_rows > 128 ? 2 : 1;
   const cudaError_t e = c->dtype == QE_BF16 ? launch_attn<__nv_bfloat16>(a, D, p.grid, (cudaStream_t)stream)
                                             : launch_attn<__half>(a, D, p.grid, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "attn_decode_step launch");

@@ -27,7 +27,8 @@ def rotate(x, pos, inv_freq, axis, adjacent):
 
 def gather(pages, page_size, list_, n, h):
     """Keys (or values) 0 .. n-1 of head h on the pages list_, [n, D]."""
-    return np.stack([pages[list_[j // page_size], h, j % page_size] for j in range(n)]) if n else np.zeros((0, pages.shape[3]))
+    j = np.arange(n)
+    return pages[np.asarray(list_, np.int64)[j // page_size], h, j % page_size] if n else np.zeros((0, pages.shape[3]))
 
 
 def attend(q, k, v, scale, dtype):

@@ -192,14 +192,11 @@ def attend_inputs(dtype, D, n_kv, G, page, prefix, lens, seed=0, cols=None, gap=
         d[n] = pool[:, :n_kv * page * D].unflatten(1, (n_kv, page, D))
         full = torch.randn((n_pages, n_kv, page, D), generator=g, device="cuda").to(dt(dtype))
         # what no row may read stays NaN: the ends of last pages, unused pages
-        for i in range(n_pre):
-            m = min(page, prefix - i * page)
-            d[n][order[i], :, :m] = full[order[i], :, :m]
-        for b in range(B):
-            for j in range(cols):
-                m = min(page, max(lens[b], 0) - j * page)
-                if m > 0:
-                    d[n][d["tb"][b, j], :, :m] = full[d["tb"][b, j], :, :m]
+        used = np.zeros(n_pages, np.int64)
+        used[order[:n_pre]] = np.clip(prefix - page * np.arange(n_pre), 0, page)
+        used[d["tb"]] = np.clip(np.maximum(np.array(lens), 0)[:, None] - page * np.arange(cols)[None, :], 0, page)
+        there = torch.from_numpy(np.arange(page)[None, :] < used[:, None]).cuda()[:, None, :, None]
+        d[n].copy_(torch.where(there, full, NAN))
     d["q"] = (scale_q * torch.randn((B, n_kv * G, D), generator=g, device="cuda")).to(dt(dtype))
     d["scale"] = 1.3 / math.sqrt(D)
     return d
@@ -256,6 +253,21 @@ ATTEND = [
     ("f16", 64, 2, 4, 8, 2049, [17] * 40),
     ("bf16", 256, 1, 8, 64, 700, [9, 0, 100] * 11),
     ("bf16", 128, 1, 1, 16, 0, [3000]),
+    # several blocks and tiles for each multiprocessor: own rows, one row a block and large groups
+    ("f16", 64, 4, 2, 16, 0, [(37 * i) % 700 for i in range(100)]),
+    ("bf16", 128, 8, 3, 32, 0, [(97 * i) % 500 for i in range(90)]),
+    ("f16", 256, 4, 4, 64, 0, [(61 * i) % 400 for i in range(90)]),
+    ("bf16", 64, 1, 70, 16, 10, [900, 0, 40]),
+    ("f16", 128, 1, 300, 16, 0, [5, 2000]),
+    ("bf16", 256, 1, 130, 16, 200, [700, 300]),
+    # prefixes of many tiles, 65 to 300 rows
+    ("f16", 64, 2, 4, 64, 20000, [(13 * i) % 90 for i in range(70)]),
+    ("bf16", 128, 2, 4, 64, 20000, [(13 * i) % 90 for i in range(70)]),
+    ("bf16", 128, 8, 2, 64, 9000, [3] * 40),
+    ("f16", 256, 2, 4, 64, 20000, [(13 * i) % 90 for i in range(33)]),
+    ("bf16", 64, 1, 1, 64, 40000, [200] * 66),
+    # more blocks of the prefix's rows than multiprocessors
+    ("f16", 64, 1, 16, 16, 200, [1] * 2600),
 ]
 
 
