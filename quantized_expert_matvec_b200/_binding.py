@@ -393,45 +393,64 @@ def gdn_decode_step(state, q, k, v, alpha, beta, out, stream=None):
                                _ptr(out), _stream(stream)))
 
 
-def _code(dtype):
+# What the attn_* and token_sample calls need of torch, looked up at their first
+# use: a decode step makes these calls once a layer, and a call's host time
+# counts as much as the kernel's.
+_torch = _raw_stream = _device = None
+_CODES = {}
+
+
+def _lazy():
+    global _torch, _raw_stream, _device
     import torch
+    _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _CODES.update({torch.float32: QE_F32, torch.bfloat16: QE_BF16, torch.float16: QE_F16})
+    torch.cuda.current_device()  # initialises CUDA
+    _torch = torch
+
+
+def _code(dtype):
     try:
-        return {torch.float32: QE_F32, torch.bfloat16: QE_BF16, torch.float16: QE_F16}[dtype]
+        return _CODES[dtype]
     except KeyError:
         raise ValueError(f"expected float32, bfloat16 or float16, got {dtype}") from None
 
 
-def _here(name, t, dtype=None, shape=None, dev=None):
-    """Data pointer of a CUDA tensor of the current device, after its dtype and
-    shape were checked; its strides are the caller's matter."""
+def _placed(name, t, dtype, dev):
+    """Raises for a tensor of another dtype or not on the current device."""
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != dev:
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _vec(name, t, dtype, n, dev):
+    """Pointer of an optional dense tensor of n elements (n None: any number)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or (n is not None and t.numel() != n) or not t.is_contiguous():
+        _placed(name, t, dtype, dev)
+        if n is not None and t.numel() != n:
+            raise ValueError(f"{name} must have {n} elements, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _vec(name, t, dtype, shape, dev):
-    """As _here, for an optional dense tensor."""
-    if t is None:
-        return None
-    p = _here(name, t, dtype, shape, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return p
-
-
-def _heads(name, t, dtype, heads, dim, dev):
+def _heads(name, t, dtype, T, heads, dim, dev):
     """Pointer and token stride of [T, heads, dim] with dense heads."""
-    p = _here(name, t, dtype, (t.shape[0], heads, dim), dev)
     s = t.stride()
-    if (heads > 1 and s[1] != dim) or s[2] != 1:
+    if t.shape != (T, heads, dim) or t.get_device() != dev or t.dtype is not dtype or s[2] != 1 or (heads > 1 and s[1] != dim):
+        _placed(name, t, dtype, dev)
+        if t.shape != (T, heads, dim):
+            raise ValueError(f"{name} must have shape {(T, heads, dim)}, got {tuple(t.shape)}")
         raise ValueError(f"the heads of {name} must be dense")
-    return p, s[0]
+    return t.data_ptr(), s[0]
+
+
+def _on(stream, dev):
+    return _raw_stream(dev) if stream is None else _stream(stream)
 
 
 class KVCache:
@@ -441,6 +460,8 @@ class KVCache:
 
     def __init__(self, k, v):
         import torch
+        if _torch is None and k.is_cuda:
+            _lazy()
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
             raise ValueError("k and v must be [n_pages, n_kv, page_size, head_dim] of one dtype and device")
         if not k.is_cuda:
@@ -457,6 +478,7 @@ class KVCache:
         self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), k.stride(0) if n > 1 else page, v.stride(0) if n > 1 else page,
                                 n, p, h, d, _code(k.dtype), 0)
         self._ref = ctypes.byref(self.desc)
+        self._dev = k.get_device()
 
 
 class Rope:
@@ -504,29 +526,29 @@ def attn_kv_append(cache: KVCache, q, k, v, table, kv_pos, q_out=None, rope: Rop
     sequence whose pages are table[seq[t]] (int32 [n_seq, columns]; seq None:
     t).  pos int32 [n_axes, T] are the rotation's positions (None: kv_pos).  q may
     be None; q_out may be q itself where the dtypes agree."""
-    import torch
-    dev, i32, D = torch.cuda.current_device(), torch.int32, cache.head_dim
-    T = k.shape[0]
-    _here("cache", cache.k, dev=dev)
-    kp, ks = _heads("k", k, None, cache.n_kv, D, dev)
-    vp, vs = _heads("v", v, k.dtype, cache.n_kv, D, dev)
+    dev, D, dtype = _device(), cache.head_dim, k.dtype
+    i32, T, n_kv = _torch.int32, k.shape[0], cache.n_kv
+    if cache._dev != dev:
+        raise ValueError(f"the cache is on cuda:{cache._dev}, the current device is cuda:{dev}")
+    kp, ks = _heads("k", k, dtype, T, n_kv, D, dev)
+    vp, vs = _heads("v", v, dtype, T, n_kv, D, dev)
     n_q, qp, qs, op, os_ = 0, None, 0, None, 0
     if q is not None:
         n_q = q.shape[1]
-        qp, qs = _heads("q", q, k.dtype, n_q, D, dev)
-        op, os_ = _heads("q_out", q_out, cache.dtype, n_q, D, dev)
-    if v.shape[0] != T or (q is not None and (q.shape[0] != T or q_out.shape[0] != T)):
-        raise ValueError("q, k, v and q_out must have the same number of tokens")
-    if table.dim() != 2:
-        raise ValueError("table must be [n_seq, columns]")
+        qp, qs = _heads("q", q, dtype, T, n_q, D, dev)
+        op, os_ = _heads("q_out", q_out, cache.dtype, T, n_q, D, dev)
+    n_seq, cols = table.shape
+    axes = 1
     if rope is not None:
-        _here("inv_freq", rope.inv_freq, dev=dev)
-    _check(lib.attn_kv_append(cache._ref, rope._ref if rope is not None else None, T, n_q, qp, kp, vp, _code(k.dtype),
-                              qs, ks, vs, op, os_,
-                              _vec("pos", pos, i32, (rope.n_axes if rope is not None else 1, T), dev),
-                              _vec("kv_pos", kv_pos, i32, (T,), dev), _vec("seq", seq, i32, (T,), dev),
-                              _vec("table", table, i32, None, dev), table.shape[0], table.shape[1],
-                              _vec("ws", ws, torch.uint8, None, dev), ws.numel(), _stream(stream)))
+        axes = rope.n_axes
+        if rope.inv_freq.get_device() != dev:
+            _placed("inv_freq", rope.inv_freq, None, dev)
+    rc = lib.attn_kv_append(cache._ref, rope._ref if rope is not None else None, T, n_q, qp, kp, vp, _code(dtype), qs, ks,
+                            vs, op, os_, _vec("pos", pos, i32, axes * T, dev), _vec("kv_pos", kv_pos, i32, T, dev),
+                            _vec("seq", seq, i32, T, dev), _vec("table", table, i32, None, dev), n_seq, cols,
+                            _vec("ws", ws, _torch.uint8, None, dev), ws.numel(), _on(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def attn_decode_step(cache: KVCache, q, out, table, kv_len, prefix_pages=None, prefix_len=0, scale=None, lse=None,
@@ -536,21 +558,25 @@ def attn_decode_step(cache: KVCache, q, out, table, kv_len, prefix_pages=None, p
     tokens on table[b] (int32 [B, columns]; kv_len negative: a padding row, left
     as it was), into out.  scale defaults to head_dim ** -0.5; lse float32
     [B, n_q] receives the logarithm of the softmax's denominator."""
-    import torch
-    dev, i32, D = torch.cuda.current_device(), torch.int32, cache.head_dim
+    dev, D, dtype = _device(), cache.head_dim, cache.dtype
+    i32 = _torch.int32
     B, n_q = q.shape[0], q.shape[1]
-    _here("cache", cache.k, dev=dev)
-    qp, qs = _heads("q", q, cache.dtype, n_q, D, dev)
-    op, os_ = _heads("out", out, cache.dtype, n_q, D, dev)
-    if out.shape[0] != B or table.dim() != 2 or table.shape[0] != B:
-        raise ValueError("q, out and table must have the same number of rows")
+    if cache._dev != dev:
+        raise ValueError(f"the cache is on cuda:{cache._dev}, the current device is cuda:{dev}")
+    qp, qs = _heads("q", q, dtype, B, n_q, D, dev)
+    op, os_ = _heads("out", out, dtype, B, n_q, D, dev)
+    rows, cols = table.shape
+    if rows != B:
+        raise ValueError(f"table must have {B} rows, got {rows}")
     if prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() * cache.page_size < prefix_len):
         raise ValueError("prefix_pages must hold prefix_len tokens")
-    _check(lib.attn_decode_step(cache._ref, B, n_q, qp, qs, _vec("prefix_pages", prefix_pages, i32, None, dev),
-                                prefix_len, _vec("table", table, i32, None, dev), table.shape[1],
-                                _vec("kv_len", kv_len, i32, (B,), dev), D ** -0.5 if scale is None else scale, op, os_,
-                                _vec("lse", lse, torch.float32, (B, n_q), dev), _vec("ws", ws, torch.uint8, None, dev),
-                                ws.numel(), _stream(stream)))
+    rc = lib.attn_decode_step(cache._ref, B, n_q, qp, qs, _vec("prefix_pages", prefix_pages, i32, None, dev), prefix_len,
+                              _vec("table", table, i32, None, dev), cols, _vec("kv_len", kv_len, i32, B, dev),
+                              D ** -0.5 if scale is None else scale, op, os_,
+                              _vec("lse", lse, _torch.float32, B * n_q, dev), _vec("ws", ws, _torch.uint8, None, dev),
+                              ws.numel(), _on(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def token_sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None, stream=None):
@@ -558,14 +584,19 @@ def token_sample(logits, u, token, temperature=None, top_k=None, top_p=None, min
     (float32 [B]) into token (int32 [B]): temperature, top_p, min_p float32 [B]
     and top_k int32 [B], each None for "off"; logprob float32 [B] receives the
     logarithm of the chosen token's probability among those kept."""
-    import torch
-    dev, i32, f32 = torch.cuda.current_device(), torch.int32, torch.float32
-    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
-        raise ValueError("logits must be [B, V] with dense rows")
+    if _torch is None:
+        _lazy()
+    dev, f32 = _device(), _torch.float32
     B, V = logits.shape
-    n = (B,)
-    _check(lib.token_sample(_here("logits", logits, dev=dev), _code(logits.dtype), B, V, logits.stride(0),
-                            _vec("temperature", temperature, f32, n, dev), _vec("top_k", top_k, i32, n, dev),
-                            _vec("top_p", top_p, f32, n, dev), _vec("min_p", min_p, f32, n, dev),
-                            _vec("u", u, f32, n, dev), _vec("token", token, i32, n, dev),
-                            _vec("logprob", logprob, f32, n, dev), _stream(stream)))
+    s = logits.stride()
+    if s[1] != 1 and V > 1:
+        raise ValueError("logits must be [B, V] with dense rows")
+    if logits.get_device() != dev:
+        _placed("logits", logits, None, dev)
+    rc = lib.token_sample(logits.data_ptr(), _code(logits.dtype), B, V, s[0], _vec("temperature", temperature, f32, B, dev),
+                          _vec("top_k", top_k, _torch.int32, B, dev), _vec("top_p", top_p, f32, B, dev),
+                          _vec("min_p", min_p, f32, B, dev), _vec("u", u, f32, B, dev),
+                          _vec("token", token, _torch.int32, B, dev), _vec("logprob", logprob, f32, B, dev),
+                          _on(stream, dev))
+    if rc:
+        _check(rc)
