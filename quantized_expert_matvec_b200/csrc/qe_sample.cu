@@ -17,11 +17,20 @@
 // The row is read once.  A cluster of CTAs shares it, each holding a run of the
 // row as stored in its shared memory; a thread owns an odd number of
 // consecutive 16-byte pieces, so that threads are in index order (which the
-// running sums need) and their 16-byte reads fall on different banks.  The
-// cuts need no sort: a histogram of 2048 bins over x_max - x (7 mantissa bits of 16
-// binades), summed over the cluster through distributed shared memory, gives
-// the bin in which the k-th token or the top_p mass lies; further histograms
-// over the bin's order-preserving keys, 11 bits at a time, give the key itself.
+// running sums need) and their 16-byte reads fall on different banks.
+//
+// What costs time is the weights (a dozen fp64 operations each) and the
+// cluster's barriers, so both are avoided:
+//   - candidates: a bound on x_max - x that holds for every token that can be
+//     kept comes from min_p, from a histogram of the threads' largest logits (the
+//     k-th largest of them is at most the k-th largest logit), or from a histogram
+//     of the weights over x_max - x.  Up to 1024 candidates are gathered, in index
+//     order, by the first CTA, which sorts them and finishes alone;
+//   - otherwise the cut is found without a sort: the histogram (1024 bins, 7
+//     mantissa bits of 8 binades), summed over the cluster through distributed
+//     shared memory, gives the bin in which the k-th token or the top_p mass
+//     lies; further histograms over the bin's order-preserving keys, 10 bits at a
+//     time, give the key itself.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -41,7 +50,9 @@ typedef unsigned long long u64;
 
 constexpr int kSampleThreads = 512;
 constexpr int kSampleWarps = kSampleThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 1024;
+constexpr int kBinBias = (127 - 3) << 7;  // bin 0: x_max - x below 2^-3 (1 + 2^-7); the last: from 2^5 on
+constexpr int kMaxCand = 1024;
 constexpr int kMaxVocab = 1 << 19;
 constexpr int kMaxCluster = 16;
 
@@ -69,8 +80,17 @@ struct SampleShared {
   double exp2_table[kExpTable];
   u64 xch[2][kMaxCluster];   // all-gather slots, two in turn
   u64 warp_sum[kSampleWarps];
-  u64 found[2][4];           // crossing bin, sum above it, its own sum
-  unsigned hist[3][kBins];   // 16-bit pieces of the weights' sums
+  u64 found[2][2];           // crossing bin and sum above it
+  union {
+    struct {
+      unsigned piece[3][kBins];  // 16-bit pieces of the weights' sums
+      u64 sum[kBins];            // put together
+    } hist;
+    struct {
+      u64 cand[kMaxCand];   // {index, logit} in index order
+      u64 order[kMaxCand];  // {key, ~place} to be sorted
+    } few;
+  };
 };
 
 QE_DEV uint32_t cluster_rank() {
@@ -96,9 +116,9 @@ QE_DEV uint32_t peer_addr(const void* p, uint32_t rank) {
   return a;
 }
 QE_DEV void st_peer64(uint32_t a, u64 v) { asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory"); }
-QE_DEV uint32_t ld_peer32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+QE_DEV u64 ld_peer64(uint32_t a) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
 }
 
@@ -173,6 +193,7 @@ struct Row {
     }
   }
 
+  QE_DEV bool each_any() const { return (int)threadIdx.x * per_thread < pieces; }  // has this thread elements
   // Every CTA's v, by rank, in the returned array (valid until the next but one call).
   QE_DEV const u64* all_gather(u64 v) {
     u64* slots = sh.xch[turn];
@@ -181,21 +202,6 @@ struct Row {
     cluster_sync();
     return slots;
   }
-  QE_DEV u64 block_sum(u64 v) {
-    v += __shfl_xor_sync(0xffffffffu, v, 16);
-    v += __shfl_xor_sync(0xffffffffu, v, 8);
-    v += __shfl_xor_sync(0xffffffffu, v, 4);
-    v += __shfl_xor_sync(0xffffffffu, v, 2);
-    v += __shfl_xor_sync(0xffffffffu, v, 1);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh.warp_sum[threadIdx.x >> 5] = v;
-    __syncthreads();
-    u64 s = 0;
-#pragma unroll
-    for (int w = 0; w < kSampleWarps; ++w) s += sh.warp_sum[w];
-    return s;
-  }
-
   // Weight of a logit as a multiple of 2^-S: e^y = 2^(k / 128) e^r with
   // k = rint(128 y / ln 2) and |r| <= ln 2 / 256, where four terms after 1
   // leave r^5 / 120 = 1.2e-15.  The product is below 2^52, so adding 2^52
@@ -222,130 +228,151 @@ struct Row {
 
   QE_DEV int coarse_bin(float x) const {
     if (!(x < x_max)) return x == x_max ? 0 : kBins - 1;
-    const int b = (int)(__float_as_uint(x_max - x) >> 16) - ((127 - 8) << 7);
+    const int b = (int)(__float_as_uint(x_max - x) >> 16) - kBinBias;
     return min(max(b, 0), kBins - 1);
+  }
+  // Upper end of a bin's x_max - x; infinity for the last.
+  QE_DEV static float bin_end(int bin) {
+    return bin == kBins - 1 ? INFINITY : __uint_as_float((uint32_t)(bin + 1 + kBinBias) << 16);
   }
 
   // Zeroes the histogram; a barrier has to follow before the first add.
   QE_DEV void hist_clear() {
-    for (int i = threadIdx.x; i < 3 * kBins; i += kSampleThreads) (&sh.hist[0][0])[i] = 0;
+    for (int i = threadIdx.x; i < 3 * kBins; i += kSampleThreads) (&sh.hist.piece[0][0])[i] = 0;
   }
   QE_DEV void hist_add(int bin, u64 w) {
     const unsigned lo = (unsigned)w & 0xffffu, mid = (unsigned)(w >> 16) & 0xffffu, hi = (unsigned)(w >> 32);
-    if (lo) atomicAdd(&sh.hist[0][bin], lo);
-    if (mid) atomicAdd(&sh.hist[1][bin], mid);
-    if (hi) atomicAdd(&sh.hist[2][bin], hi);
+    if (lo) atomicAdd(&sh.hist.piece[0][bin], lo);
+    if (mid) atomicAdd(&sh.hist.piece[1][bin], mid);
+    if (hi) atomicAdd(&sh.hist.piece[2][bin], hi);
   }
-  // The bin in which the cluster's sum, bin 0 first, reaches `target` (1 <=
-  // target <= the total); above: the sum before it.  All CTAs get it.
-  QE_DEV int crossing(u64 target, u64* above) {
-    cluster_sync();  // every CTA's histogram is complete
-    const int per = kBins / size;  // size is a power of two
-    constexpr int kMost = kBins / kSampleThreads;
-    u64 v[kMost];
+  // The cluster's histogram, in slices: thread t of CTA r gets the sums of the bins
+  // first_bin() ..., their running sum before them and the total.
+  struct Sums {
+    u64 v[kBins / kSampleThreads], before, total;
+  };
+  QE_DEV int slice() const { return kBins / size; }  // size is a power of two
+  QE_DEV int per_slot() const { return slice() >= kSampleThreads ? slice() / kSampleThreads : 1; }
+  QE_DEV Sums hist_sums() {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kSampleThreads)
+      sh.hist.sum[i] = (u64)sh.hist.piece[0][i] + ((u64)sh.hist.piece[1][i] << 16) + ((u64)sh.hist.piece[2][i] << 32);
+    cluster_sync();  // every CTA's sums are there
+    Sums s;
+    const int m = per_slot();
     u64 sum = 0;
-    const int b0 = rank * per;
-    // thread t: bins [t * m, (t + 1) * m) of this CTA's slice
-    const int m = per >= kSampleThreads ? per / kSampleThreads : 1;
 #pragma unroll
-    for (int j = 0; j < kMost; ++j) {
-      v[j] = 0;
+    for (int j = 0; j < kBins / kSampleThreads; ++j) {
+      s.v[j] = 0;
       const int i = threadIdx.x * m + j;
-      if (j < m && i < per)
-        for (uint32_t r = 0; r < size; ++r) {
-          v[j] += (u64)ld_peer32(peer_addr(&sh.hist[0][b0 + i], r));
-          v[j] += (u64)ld_peer32(peer_addr(&sh.hist[1][b0 + i], r)) << 16;
-          v[j] += (u64)ld_peer32(peer_addr(&sh.hist[2][b0 + i], r)) << 32;
-        }
-      sum += v[j];
+      if (j < m && i < slice()) {
+        u64 x[4] = {0, 0, 0, 0};
+        for (uint32_t r = 0; r < size; r += 4)
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k)
+            if (r + k < size) x[k] += ld_peer64(peer_addr(&sh.hist.sum[rank * slice() + i], r + k));
+        s.v[j] = (x[0] + x[1]) + (x[2] + x[3]);
+      }
+      sum += s.v[j];
     }
     u64 scan = warp_scan(sum);
     __syncthreads();
     if ((threadIdx.x & 31) == 31) sh.warp_sum[threadIdx.x >> 5] = scan;
     __syncthreads();
-    u64 total = 0;
+    u64 all = 0;
 #pragma unroll
     for (int w = 0; w < kSampleWarps; ++w) {
       if (w < (int)(threadIdx.x >> 5)) scan += sh.warp_sum[w];
-      total += sh.warp_sum[w];
+      all += sh.warp_sum[w];
     }
-    const u64* slices = all_gather(total);
-    u64 before = scan - sum;
-    for (uint32_t r = 0; r < rank; ++r) before += slices[r];
+    const u64* slices = all_gather(all);
+    s.before = scan - sum;
+    s.total = 0;
+    for (uint32_t r = 0; r < size; ++r) {
+      if (r < rank) s.before += slices[r];
+      s.total += slices[r];
+    }
+    return s;
+  }
+  // The bin in which the sums, bin 0 first, reach `target` (1 <= target <= the
+  // total); above: the sum before it.  All CTAs get it.
+  QE_DEV int crossing(const Sums& s, u64 target, u64* above) {
     u64* out = sh.found[turn_found];
     turn_found ^= 1;
+    u64 before = s.before;
 #pragma unroll
-    for (int j = 0; j < kMost; ++j) {
-      if (before < target && target <= before + v[j])
+    for (int j = 0; j < kBins / kSampleThreads; ++j) {
+      if (before < target && target <= before + s.v[j])
         for (uint32_t r = 0; r < size; ++r) {
-          st_peer64(peer_addr(out, r), (u64)(b0 + threadIdx.x * m + j));
+          st_peer64(peer_addr(out, r), (u64)(rank * slice() + threadIdx.x * per_slot() + j));
           st_peer64(peer_addr(out + 1, r), before);
         }
-      before += v[j];
+      before += s.v[j];
     }
     cluster_sync();
     *above = out[1];
     return (int)out[0];
   }
 
-  // Smallest index i with sum_{j <= i} w(x_j, j) > target, given that the
-  // row's total exceeds target; all threads of all CTAs get it.
+  // Sum of w over the row; mine, before: this thread's part and what comes before it.
   template <typename F>
-  QE_DEV int locate(F w, u64 target) {
-    u64 mine = 0;
-    each([&](float x, int i) { mine += w(x, i); });
-    u64 scan = warp_scan(mine);
+  QE_DEV u64 running(F w, u64* mine, u64* before) {
+    u64 m = 0;
+    each([&](float x, int i) { m += w(x, i); });
+    u64 scan = warp_scan(m);
     __syncthreads();
     if ((threadIdx.x & 31) == 31) sh.warp_sum[threadIdx.x >> 5] = scan;
     __syncthreads();
-    u64 total = 0;
+    u64 all = 0;
 #pragma unroll
     for (int k = 0; k < kSampleWarps; ++k) {
       if (k < (int)(threadIdx.x >> 5)) scan += sh.warp_sum[k];
-      total += sh.warp_sum[k];
+      all += sh.warp_sum[k];
     }
-    const u64* runs = all_gather(total);
-    u64 before = scan - mine;
-    for (uint32_t r = 0; r < rank; ++r) before += runs[r];
-    u64* out = sh.found[turn_found];
-    turn_found ^= 1;
-    if (before <= target && target < before + mine) {
-      int at = -1;
-      each([&](float x, int i) {
-        before += w(x, i);
-        if (at < 0 && before > target) at = i;
-      });
-      for (uint32_t r = 0; r < size; ++r) st_peer64(peer_addr(out, r), (u64)at);
+    const u64* runs = all_gather(all);
+    u64 b = scan - m, total = 0;
+    for (uint32_t r = 0; r < size; ++r) {
+      if (r < rank) b += runs[r];
+      total += runs[r];
     }
-    cluster_sync();
-    return (int)out[0];
+    *mine = m;
+    *before = b;
+    return total;
+  }
+  // In the warp in one of whose threads' parts the running sum exceeds `target` (below
+  // the total): the first such index; -1 in the others.  The warp shares that part out.
+  template <typename F>
+  QE_DEV int place_of(F w, u64 mine, u64 before, u64 target) const {
+    const unsigned owner = __ballot_sync(0xffffffffu, before <= target && target < before + mine);
+    if (!owner) return -1;
+    const int src = __ffs(owner) - 1, lane = threadIdx.x & 31, p0 = ((threadIdx.x & ~31) + src) * per_thread;
+    const int end = min(pieces, p0 + per_thread) * N;
+    u64 base = __shfl_sync(0xffffffffu, before, src);
+    for (int e0 = p0 * N; e0 < end; e0 += 32) {
+      const int e = e0 + lane;
+      const u64 scan = base + warp_scan(e < end ? w((float)reinterpret_cast<const T*>(data)[e], first + e) : 0);
+      const unsigned past = __ballot_sync(0xffffffffu, scan > target);
+      if (past) return first + e0 + __ffs(past) - 1;
+      base = __shfl_sync(0xffffffffu, scan, 31);
+    }
+    return -1;
   }
 
   // Cuts the kept elements, in descending order, to the shortest run whose sum
   // of w reaches target (1 <= target <= their sum).  w is 0 for what is not kept.
   template <typename F>
-  QE_DEV void cut_at(F w, u64 target) {
-    hist_clear();
-    __syncthreads();
-    each([&](float x, int i) {
-      const u64 v = w(x, i);
-      if (v) hist_add(coarse_bin(x), v);
-    });
-    u64 above;
-    const int bin = crossing(target, &above);
-    target -= above;
-    // keys that the bin can hold: its bounds on x_max - x, widened by two
+  QE_DEV void cut_at(F w, int bin, u64 target) {
+    // bin: the coarse bin that the run ends in; target: what is to be reached within it.
+    // Keys that the bin can hold: its bounds on x_max - x, widened by two
     // units in the last place of that difference
     uint32_t k_hi = key_of(x_max), k_lo = key_of(-INFINITY);
-    const double d_lo = (double)__uint_as_float((uint32_t)(bin + ((127 - 8) << 7)) << 16);
-    const double d_hi = (double)__uint_as_float((uint32_t)(bin + 1 + ((127 - 8) << 7)) << 16);
+    const double d_lo = (double)__uint_as_float((uint32_t)(bin + kBinBias) << 16), d_hi = (double)bin_end(bin);
     if (bin > 0) k_hi = min(k_hi, key_of(__double2float_ru((double)x_max - d_lo * (1.0 - 2.4e-7))));
-    if (bin < kBins - 1 && x_max < INFINITY) k_lo = key_of(__double2float_rd((double)x_max - d_hi * (1.0 + 2.4e-7)));
-    if (bin < kBins - 1 && x_max == INFINITY) k_lo = k_hi;
+    if (bin < kBins - 1) k_lo = x_max < INFINITY ? key_of(__double2float_rd((double)x_max - d_hi * (1.0 + 2.4e-7))) : k_hi;
     for (;;) {
       const uint32_t range = k_hi - k_lo;
       const int bits = 32 - __clz(range | 1);
-      const int sh_bits = bits > 11 ? bits - 11 : 0;
+      const int sh_bits = bits > 10 ? bits - 10 : 0;
       hist_clear();  // crossing() ends well after the last peer's read
       __syncthreads();
       each([&](float x, int i) {
@@ -354,7 +381,9 @@ struct Row {
         const u64 v = w(x, i);
         if (v) hist_add((int)((k_hi - k) >> sh_bits), v);
       });
-      const int b = crossing(target, &above);
+      u64 above;
+      const Sums sums = hist_sums();
+      const int b = crossing(sums, target, &above);
       target -= above;
       k_hi -= (uint32_t)b << sh_bits;
       if (sh_bits == 0) break;
@@ -363,20 +392,141 @@ struct Row {
     }
     // of the elements with key k_hi, as many of the lowest indices as it takes
     auto tie = [&](float x, int i) -> u64 { return key_of(x) == k_hi ? w(x, i) : 0; };
-    u64 mine = 0;
-    each([&](float x, int i) { mine += tie(x, i); });
-    const u64* runs = all_gather(block_sum(mine));
-    u64 all = 0;
-    for (uint32_t r = 0; r < size; ++r) all += runs[r];
+    u64 mine, before;
+    const u64 all = running(tie, &mine, &before);
     int at = thr == k_hi ? cut : 0x7fffffff;
     if (all > target) {
-      const int last = locate(tie, target - 1);  // the run ends with the tie that reaches the target
-      at = min(at, last + 1);
+      const int last = place_of(tie, mine, before, target - 1);  // the tie that reaches the target
+      u64* out = sh.found[turn_found];
+      turn_found ^= 1;
+      if (last >= 0 && (threadIdx.x & 31) < size) st_peer64(peer_addr(out, threadIdx.x & 31), (u64)last);
+      cluster_sync();
+      at = min(at, (int)out[0] + 1);
     }
     thr = k_hi;
     cut = at;
   }
 };
+
+// floor(x total) for an fp32 0 < x < 1, exactly; rest: whether something was cut off.
+QE_DEV u64 part_of(float x, u64 total, bool* rest) {
+  int e;
+  const u64 f = (u64)(frexpf(x, &e) * 16777216.f);  // x = f 2^-s
+  const int s = 24 - e;
+  const u64 hi = __umul64hi(f, total), lo = f * total;
+  if (s < 64) {
+    *rest = (lo & (((u64)1 << s) - 1)) != 0;
+    return (hi << (64 - s)) | (lo >> s);
+  }
+  if (s < 128) {
+    *rest = lo != 0 || (s > 64 && (hi & (((u64)1 << (s - 64)) - 1)) != 0);
+    return s == 64 ? hi : hi >> (s - 64);
+  }
+  *rest = true;
+  return 0;
+}
+// The least whole number that is at least top_p total, and at least 1.
+QE_DEV u64 mass_target(float top_p, u64 total) {
+  if (!(top_p > 0.f)) return 1;
+  bool rest;
+  u64 t = part_of(top_p, total, &rest);
+  if (rest) ++t;
+  return t < 1 ? 1 : t;
+}
+QE_DEV u64 choice_target(float u, u64 total) {
+  if (u >= 1.f) return total - 1;
+  if (!(u > 0.f)) return 0;
+  bool rest;
+  return part_of(u, total, &rest);
+}
+
+// The cuts and the choice among n <= kMaxCand candidates in index order, by one CTA.
+// target_p: the mass that top_p keeps, where that is known already (no top_k).
+template <typename T>
+QE_DEV void finish_few(const Row<T>& r, int n, int top_k, bool cut_p, float top_p, u64 target_p, u64 least, float u, int row) {
+  SampleShared& sh = r.sh;
+  const SampleArgs& a = r.a;
+  constexpr int P = kMaxCand / kSampleThreads;  // places per thread
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // running sums over places, thread t having places P t ..
+  auto block_running = [&](u64 (&v)[P], u64* total) {
+#pragma unroll
+    for (int j = 1; j < P; ++j) v[j] += v[j - 1];
+    u64 scan = warp_scan(v[P - 1]);
+    __syncthreads();
+    if (lane == 31) sh.warp_sum[warp] = scan;
+    __syncthreads();
+    u64 before = scan - v[P - 1], all = 0;
+#pragma unroll
+    for (int w = 0; w < kSampleWarps; ++w) {
+      if (w < warp) before += sh.warp_sum[w];
+      all += sh.warp_sum[w];
+    }
+#pragma unroll
+    for (int j = 0; j < P; ++j) v[j] += before;
+    *total = all;
+  };
+  auto logit = [&](u64 c) { return __uint_as_float((uint32_t)c); };
+  u64 last = 0;  // the last kept candidate's {key, ~place}; all from it on are kept
+  if (top_k > 0 || cut_p) {
+    // descending by key, ascending by place: a bitonic sort of the next power of two
+    int m = 32;
+    while (m < n) m *= 2;
+    for (int i = tid; i < m; i += kSampleThreads)
+      sh.few.order[i] = i < n ? ((u64)key_of(logit(sh.few.cand[i])) << 32) | (uint32_t)~i : 0;
+    __syncthreads();
+    for (int k = 2; k <= m; k *= 2)
+      for (int j = k / 2; j > 0; j /= 2) {
+        for (int i = tid; i < m / 2; i += kSampleThreads) {
+          const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+          const u64 x = sh.few.order[lo], y = sh.few.order[hi];
+          if ((x < y) == ((lo & k) == 0)) {
+            sh.few.order[lo] = y;
+            sh.few.order[hi] = x;
+          }
+        }
+        __syncthreads();
+      }
+    int keep = top_k > 0 && top_k < n ? top_k : n;
+    if (cut_p) {
+      u64 v[P], w[P], total;
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        const int i = P * tid + j;
+        w[j] = v[j] = i < keep ? r.weight(logit(sh.few.cand[(uint32_t)~sh.few.order[i]])) : 0;
+      }
+      block_running(v, &total);
+      const u64 target = top_k > 0 ? mass_target(top_p, total) : target_p;
+#pragma unroll
+      for (int j = 0; j < P; ++j)
+        if (v[j] - w[j] < target && target <= v[j]) sh.found[0][0] = P * tid + j + 1;
+      if (tid == 0 && target > total) sh.found[0][0] = keep;  // the mass is reached below min_p
+      __syncthreads();
+      keep = (int)sh.found[0][0];
+    }
+    last = sh.few.order[keep - 1];
+  }
+  u64 v[P], w[P], total;
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    const int i = P * tid + j;
+    u64 x = 0;
+    if (i < n) {
+      const float l = logit(sh.few.cand[i]);
+      if ((((u64)key_of(l) << 32) | (uint32_t)~i) >= last) x = r.weight(l);
+      if (x < least) x = 0;
+    }
+    w[j] = v[j] = x;
+  }
+  block_running(v, &total);
+  const u64 target = choice_target(u, total);
+#pragma unroll
+  for (int j = 0; j < P; ++j)
+    if (v[j] - w[j] <= target && target < v[j]) {
+      a.token[row] = (int)(sh.few.cand[P * tid + j] >> 32);
+      if (a.logprob) a.logprob[row] = (float)log((double)w[j] / (double)total);
+    }
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleArgs a) {
@@ -419,33 +569,23 @@ __global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleA
     __syncthreads();
   }
 
-  // the largest logit, the lowest index of its ties
+  // the largest logit
   float best = -INFINITY;
-  int best_i = 0x7fffffff;
-  r.each([&](float x, int i) {
-    if (x > best) {
-      best = x;
-      best_i = i;
-    }
-  });
-  u64 top = ((u64)key_of(best) << 32) | (uint32_t)~best_i;
+  r.each([&](float x, int) { best = fmaxf(best, x); });  // NaN loses
+  u64 top = key_of(best);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    const u64 x = __shfl_xor_sync(0xffffffffu, top, d);
-    top = x > top ? x : top;
-  }
+  for (int d = 16; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
   if ((threadIdx.x & 31) == 0) sh.warp_sum[threadIdx.x >> 5] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kSampleWarps; ++w) top = sh.warp_sum[w] > top ? sh.warp_sum[w] : top;
+  for (int w = 0; w < kSampleWarps; ++w) top = max(top, sh.warp_sum[w]);
   cluster_wait();
   const u64* tops = r.all_gather(top);
-  for (uint32_t k = 0; k < r.size; ++k) top = tops[k] > top ? tops[k] : top;
-  const uint32_t k_max = (uint32_t)(top >> 32);
+  for (uint32_t k = 0; k < r.size; ++k) top = max(top, tops[k]);
+  const uint32_t k_max = (uint32_t)top;
   r.x_max = __uint_as_float(k_max & 0x80000000u ? k_max ^ 0x80000000u : ~k_max);
-  const bool first = r.rank == 0 && threadIdx.x == 0;
   if (r.x_max == -INFINITY) {  // nothing to choose from
-    if (first) {
+    if (r.rank == 0 && threadIdx.x == 0) {
       a.token[row] = -1;
       if (a.logprob) a.logprob[row] = -INFINITY;
     }
@@ -453,94 +593,118 @@ __global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleA
     return;
   }
   const float t = a.temperature ? a.temperature[row] : 1.f;
-  if (!(t > 0.f)) {  // greedy
-    if (first) {
-      a.token[row] = (int)~(uint32_t)top;
+  const int k = a.top_k ? a.top_k[row] : 0;
+  const float tp = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f, u = a.u[row];
+  u64 mine, before;
+  if (!(t > 0.f)) {  // greedy: the first of the largest
+    auto largest = [&](float x, int) -> u64 { return x == r.x_max; };
+    r.running(largest, &mine, &before);
+    const int at = r.place_of(largest, mine, before, 0);
+    if (at >= 0 && (threadIdx.x & 31) == 0) {
+      a.token[row] = at;
       if (a.logprob) a.logprob[row] = 0.f;
     }
     cluster_sync();
     return;
   }
   r.inv_t = 1.0 / (double)t;
+  u64 least = 1;  // of a kept weight
+  if (mp > 0.f) least = max((u64)1, (u64)ceil((double)fminf(mp, 1.f) * (double)((u64)1 << a.shift)));
+  const bool cut_k = k > 0 && k < a.V, cut_p = tp < 1.f;
 
-  const int k = a.top_k ? a.top_k[row] : 0;
-  if (k > 0 && k < a.V) r.cut_at([&](float, int i) -> u64 { return i >= i0 && i < i1 ? 1 : 0; }, (u64)k);
-  auto mass = [&](float x, int i) -> u64 { return r.kept(x, i) ? r.weight(x) : 0; };
-  const float tp = a.top_p ? a.top_p[row] : 1.f;
-  if (tp < 1.f) {
-    u64 mine = 0;
-    r.each([&](float x, int i) { mine += mass(x, i); });
-    const u64* runs = r.all_gather(r.block_sum(mine));
-    u64 total = 0;
-    for (uint32_t j = 0; j < r.size; ++j) total += runs[j];
-    // the least whole number that is at least top_p total: top_p = f 2^-e
-    // with a 24-bit f, total below 2^63
-    u64 target = 1;
-    if (tp > 0.f) {
-      int e;
-      const u64 f = (u64)(frexpf(tp, &e) * 16777216.f);
-      const int s = 24 - e;  // top_p = f 2^-s, s >= 24
-      const u64 hi = __umul64hi(f, total), lo = f * total;
-      u64 w = 0;
-      bool rest;
-      if (s < 64) {
-        w = (hi << (64 - s)) | (lo >> s);
-        rest = (lo & (((u64)1 << s) - 1)) != 0;
-      } else if (s < 128) {
-        w = s == 64 ? hi : hi >> (s - 64);
-        rest = lo != 0 || (s > 64 && (hi & (((u64)1 << (s - 64)) - 1)) != 0);
-      } else {
-        rest = true;
-      }
-      target = w + (rest ? 1 : 0);
-      if (target < 1) target = 1;
-    }
-    r.cut_at(mass, target);
+  // A bound on x_max - x for the candidates, all tokens that can be kept
+  float far = INFINITY;
+  int bin = kBins - 1;
+  u64 target_p = 0, above = 0;
+  if (cut_k) {
+    r.hist_clear();
+    __syncthreads();
+    if (r.each_any()) atomicAdd(&sh.hist.piece[0][r.coarse_bin(best)], 1u);
+    const typename Row<T>::Sums sums = r.hist_sums();
+    if (sums.total >= (u64)k) far = Row<T>::bin_end(r.crossing(sums, (u64)k, &above));
+  } else if (cut_p) {
+    r.hist_clear();
+    __syncthreads();
+    r.each([&](float x, int) {
+      const u64 w = r.weight(x);
+      if (w) r.hist_add(r.coarse_bin(x), w);
+    });
+    const typename Row<T>::Sums sums = r.hist_sums();
+    target_p = mass_target(tp, sums.total);
+    bin = r.crossing(sums, target_p, &above);
+    far = Row<T>::bin_end(bin);
   }
-  const float mp = a.min_p ? a.min_p[row] : 0.f;
-  u64 least = 1;
-  if (mp > 0.f) least = (u64)ceil((double)fminf(mp, 1.f) * (double)((u64)1 << a.shift));
-  if (least < 1) least = 1;
+  // (with a top_k, top_p goes by the mass of all its tokens)
+  if (mp > 0.f && !(cut_k && cut_p)) {
+    // a kept weight is at least least - 1/2 before its rounding; 1e-6 covers the rounding of x_max - x
+    const double d = -log(((double)least - 0.5) / (double)((u64)1 << a.shift)) * (double)t;
+    far = fminf(far, __double2float_ru(d * (1.0 + 1e-6) + 1e-37));
+  }
+  if (far < INFINITY || a.V <= kMaxCand) {
+    auto near = [&](float x) { return r.x_max - x < far || x == r.x_max; };
+    const u64 n = r.running([&](float x, int) -> u64 { return near(x) ? 1 : 0; }, &mine, &before);
+    if (n <= kMaxCand) {
+      // to the first CTA, in index order
+      uint32_t to = peer_addr(sh.few.cand, 0) + (uint32_t)before * 8;
+      r.each([&](float x, int i) {
+        if (!near(x)) return;
+        st_peer64(to, ((u64)(uint32_t)i << 32) | __float_as_uint(x));
+        to += 8;
+      });
+      cluster_sync();
+      if (r.rank == 0) finish_few(r, (int)n, cut_k ? k : 0, cut_p, tp, target_p, least, u, row);
+      return;
+    }
+  }
+
+  if (cut_k) {
+    auto one = [&](float, int i) -> u64 { return i >= i0 && i < i1 ? 1 : 0; };
+    r.hist_clear();
+    __syncthreads();
+    r.each([&](float x, int i) {
+      if (one(x, i)) atomicAdd(&sh.hist.piece[0][r.coarse_bin(x)], 1u);
+    });
+    const typename Row<T>::Sums sums = r.hist_sums();
+    bin = r.crossing(sums, (u64)k, &above);
+    r.cut_at(one, bin, (u64)k - above);
+  }
+  auto mass = [&](float x, int i) -> u64 { return r.kept(x, i) ? r.weight(x) : 0; };
+  if (cut_p) {
+    if (cut_k) {
+      r.hist_clear();
+      __syncthreads();
+      r.each([&](float x, int i) {
+        const u64 w = mass(x, i);
+        if (w) r.hist_add(r.coarse_bin(x), w);
+      });
+      const typename Row<T>::Sums sums = r.hist_sums();
+      target_p = mass_target(tp, sums.total);
+      bin = r.crossing(sums, target_p, &above);
+    }
+    r.cut_at(mass, bin, target_p - above);
+  }
   auto final_mass = [&](float x, int i) -> u64 {
     const u64 w = mass(x, i);
     return w >= least ? w : 0;
   };
-  u64 mine = 0;
-  r.each([&](float x, int i) { mine += final_mass(x, i); });
-  const u64* runs = r.all_gather(r.block_sum(mine));
-  u64 total = 0;
-  for (uint32_t j = 0; j < r.size; ++j) total += runs[j];
-  // floor(u total), exactly: u = f 2^-s
-  const float uu = a.u[row];
-  u64 target = 0;
-  if (uu >= 1.f) {
-    target = total - 1;
-  } else if (uu > 0.f) {
-    int e;
-    const u64 f = (u64)(frexpf(uu, &e) * 16777216.f);
-    const int s = 24 - e;
-    const u64 hi = __umul64hi(f, total), lo = f * total;
-    target = s < 64 ? (hi << (64 - s)) | (lo >> s) : s < 128 ? (s == 64 ? hi : hi >> (s - 64)) : 0;
-  }
-  const int token = r.locate(final_mass, target);
-  if (token >= i0 && token < i1) {
-    const int local = token - r.first;
-    if (threadIdx.x == local / N / r.per_thread) {
-      const float x = (float)reinterpret_cast<const T*>(smem)[local];
-      a.token[row] = token;
-      if (a.logprob) a.logprob[row] = (float)log((double)r.weight(x) / (double)total);
-    }
+  const u64 total = r.running(final_mass, &mine, &before);
+  const int at = r.place_of(final_mass, mine, before, choice_target(u, total));
+  if (at >= 0 && (threadIdx.x & 31) == 0) {
+    a.token[row] = at;
+    const float x = (float)reinterpret_cast<const T*>(smem)[at - r.first];
+    if (a.logprob) a.logprob[row] = (float)log((double)r.weight(x) / (double)total);
   }
   cluster_sync();
 }
 
 template <typename T>
 cudaError_t launch_sample_t(SampleArgs a, cudaStream_t s) {
-  // CTAs per row: enough that a CTA's run is short (latency) and fits in shared memory
+  // CTAs per row: enough that a CTA's run is short (few rows: latency) or that several
+  // CTAs share a multiprocessor's memory (many rows)
   const int es = (int)sizeof(T);
   int cl = 1;
   while (cl < 8 && (long long)a.V * es / cl > 32768) cl *= 2;
-  if ((long long)a.V * es / cl > 160 * 1024) cl = 16;
+  if ((long long)a.V * es / cl > 56 * 1024) cl = 16;
   a.cluster = cl;
   const int n = 16 / es;
   a.run = ((a.V + cl - 1) / cl + n - 1) / n * n;
