@@ -26,10 +26,10 @@
 //     k-th largest of them is at most the k-th largest logit), or from a histogram
 //     of the weights over x_max - x.  Up to 1024 candidates are gathered, in index
 //     order, by the first CTA, which sorts them and finishes alone;
-//   - otherwise the cut is found without a sort: the histogram (1024 bins, 7
+//   - otherwise the cut is found without a sort: the histogram (2048 bins, 8
 //     mantissa bits of 8 binades), summed over the cluster through distributed
 //     shared memory, gives the bin in which the k-th token or the top_p mass
-//     lies; further histograms over the bin's order-preserving keys, 10 bits at a
+//     lies; further histograms over the bin's order-preserving keys, 11 bits at a
 //     time, give the key itself.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,6 +38,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "qe_attn.h"
 #include "qe_device.cuh"
@@ -50,8 +51,9 @@ typedef unsigned long long u64;
 
 constexpr int kSampleThreads = 512;
 constexpr int kSampleWarps = kSampleThreads / 32;
-constexpr int kBins = 1024;
-constexpr int kBinBias = (127 - 3) << 7;  // bin 0: x_max - x below 2^-3 (1 + 2^-7); the last: from 2^5 on
+constexpr int kBinBits = 11, kBins = 1 << kBinBits;
+constexpr int kBinShift = 15;                // 8 mantissa bits of x_max - x
+constexpr int kBinBias = (127 - 3) << 8;  // bin 0: below 2^-3 (1 + 2^-8); the last: from 2^5 on
 constexpr int kMaxCand = 1024;
 constexpr int kMaxVocab = 1 << 19;
 constexpr int kMaxCluster = 16;
@@ -71,24 +73,23 @@ struct SampleArgs {
   int smem_row;  // bytes of the row's run in shared memory
 };
 
-// 2^(i / 128): the table of a table-driven exponential (Tang, "Table-driven
+// 2^(i / 32): the table of a table-driven exponential (Tang, "Table-driven
 // implementation of the exponential function in IEEE floating-point
-// arithmetic", ACM TOMS 15, 1989), filled once per CTA.
-constexpr int kExpTable = 128;
+// arithmetic", ACM TOMS 15, 1989), filled once per CTA; a copy for each pair of
+// banks, so that the lanes of a half warp never meet.
+constexpr int kExpTable = 32, kExpCopies = 16;
 
 struct SampleShared {
-  double exp2_table[kExpTable];
+  double exp2_table[kExpTable][kExpCopies];
   u64 xch[2][kMaxCluster];   // all-gather slots, two in turn
   u64 warp_sum[kSampleWarps];
-  u64 found[2][2];           // crossing bin and sum above it
+  u64 found[2][3];           // crossing bin, the sum above it and its own
   union {
-    struct {
-      unsigned piece[3][kBins];  // 16-bit pieces of the weights' sums
-      u64 sum[kBins];            // put together
-    } hist;
+    unsigned piece[3][kBins];  // histogram: sums of 16-bit pieces of the weights,
+    u64 sum[kBins];            // then put together in the same place
     struct {
       u64 cand[kMaxCand];   // {index, logit} in index order
-      u64 order[kMaxCand];  // {key, ~place} to be sorted
+      u64 order[kMaxCand];  // {key, ~place} to be sorted; the buffers of block_sort
     } few;
   };
 };
@@ -129,11 +130,13 @@ QE_DEV uint32_t key_of(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+QE_DEV float logit_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
+
 template <typename T>
 struct Elems;
 template <>
 struct Elems<float> {
-  static constexpr int N = 4;
+  static constexpr int N = 4, kKeyShift = 0;
   static QE_DEV void get(const uint4& w, float (&x)[4]) {
     x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
   }
@@ -141,7 +144,8 @@ struct Elems<float> {
 };
 template <typename T>
 struct Elems {
-  static constexpr int N = 8;
+  // a 16-bit logit as fp32 has this many low zero bits, and so has its key
+  static constexpr int N = 8, kKeyShift = std::is_same<T, __half>::value ? 13 : 16;
   static QE_DEV void get(const uint4& w, float (&x)[8]) {
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -164,6 +168,32 @@ QE_DEV u64 warp_scan(u64 v) {  // inclusive
   return v;
 }
 
+// Descending, one value a thread: a bitonic sort, by shuffles within a warp and through
+// two buffers of kSampleThreads in turn beyond it.
+template <typename V>
+QE_DEV V block_sort(V v, V* buf) {
+  const int tid = threadIdx.x;
+  int turn = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 2; k <= kSampleThreads; k *= 2)
+#pragma unroll 1
+    for (int j = k / 2; j > 0; j /= 2) {
+      V o;
+      if (j >= 32) {
+        buf[turn + tid] = v;
+        __syncthreads();
+        o = buf[turn + (tid ^ j)];
+        turn ^= kSampleThreads;
+      } else {
+        o = __shfl_xor_sync(0xffffffffu, v, j);
+      }
+      const bool larger = ((tid & j) == 0) == ((tid & k) == 0);
+      v = (o > v) == larger ? o : v;
+    }
+  return v;
+}
+
 template <typename T>
 struct Row {
   static constexpr int N = Elems<T>::N;
@@ -176,8 +206,8 @@ struct Row {
   int turn = 0, turn_found = 0;
   float x_max = 0.f;
   double inv_t = 1.0, scale = 1.0;
-  uint32_t thr = 0;    // kept: key > thr, or key == thr and index < cut
-  int cut = 0x7fffffff;
+  float thr = -INFINITY;  // kept: x > thr, or x == thr and index < cut
+  int cut = 0;
 
   QE_DEV Row(const SampleArgs& a_, SampleShared& s_) : a(a_), sh(s_) {}
 
@@ -193,7 +223,6 @@ struct Row {
     }
   }
 
-  QE_DEV bool each_any() const { return (int)threadIdx.x * per_thread < pieces; }  // has this thread elements
   // Every CTA's v, by rank, in the returned array (valid until the next but one call).
   QE_DEV const u64* all_gather(u64 v) {
     u64* slots = sh.xch[turn];
@@ -202,49 +231,49 @@ struct Row {
     cluster_sync();
     return slots;
   }
-  // Weight of a logit as a multiple of 2^-S: e^y = 2^(k / 128) e^r with
-  // k = rint(128 y / ln 2) and |r| <= ln 2 / 256, where four terms after 1
-  // leave r^5 / 120 = 1.2e-15.  The product is below 2^52, so adding 2^52
-  // rounds it to a whole number in the low bits.
+  // Weight of a logit as a multiple of 2^-S: e^y = 2^(k / 32) e^r with k the whole
+  // number nearest to 32 y / ln 2 (left in the low bits by adding 1.5 2^52) and
+  // |r| <= ln 2 / 64, where five terms after 1 leave r^6 / 720 = 2.3e-15.  The product
+  // is below 2^52, so adding 2^52 rounds it to a whole number in the low bits.  No
+  // branch: the elements of a piece are worked on side by side.  Below -45 (2^-64), and
+  // for -inf and NaN, whatever comes out is dropped.
   QE_DEV u64 weight(float x) const {
-    if (x == x_max) return (u64)1 << a.shift;
+    if (x_max == INFINITY) return x == x_max ? (u64)1 << a.shift : 0;  // the same for the whole row
     const double y = ((double)x - (double)x_max) * inv_t;
-    if (!(y > -45.0)) return 0;  // below 2^-64; NaN too
-    const double kd = rint(y * 184.66496523378731);
-    const double r = fma(-kd, 0.0054152123481245727, y);
-    const int k = (int)kd;
-    double p = fma(r, 1.0 / 24.0, 1.0 / 6.0);
+    const double km = fma(y, 46.166241308446828, 6755399441055744.0);
+    const double r = fma(6755399441055744.0 - km, 0.021660849392498291, y);
+    const int k = __double2loint(km);
+    double p = fma(r, 1.0 / 120.0, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
     p = fma(p, r, 0.5);
     p = fma(p, r, 1.0);
     p = fma(p, r, 1.0);
-    p *= sh.exp2_table[k & (kExpTable - 1)];
-    const double two = __longlong_as_double((long long)(1023 + a.shift + (k >> 7)) << 52);
-    return (u64)__double_as_longlong(fma(p, two, 4503599627370496.0)) & 0xfffffffffffffull;
+    p *= sh.exp2_table[k & (kExpTable - 1)][threadIdx.x % kExpCopies];
+    const double two = __hiloint2double((1023 + a.shift + (k >> 5)) << 20, 0);
+    const u64 w = (u64)__double_as_longlong(fma(p, two, 4503599627370496.0)) & 0xfffffffffffffull;
+    return y > -45.0 ? w : 0;
   }
-  QE_DEV bool kept(float x, int i) const {
-    const uint32_t k = key_of(x);
-    return k > thr || (k == thr && i < cut);
-  }
+  QE_DEV bool kept(float x, int i) const { return x > thr || (x == thr && i < cut); }
 
   QE_DEV int coarse_bin(float x) const {
     if (!(x < x_max)) return x == x_max ? 0 : kBins - 1;
-    const int b = (int)(__float_as_uint(x_max - x) >> 16) - kBinBias;
+    const int b = (int)(__float_as_uint(x_max - x) >> kBinShift) - kBinBias;
     return min(max(b, 0), kBins - 1);
   }
   // Upper end of a bin's x_max - x; infinity for the last.
   QE_DEV static float bin_end(int bin) {
-    return bin == kBins - 1 ? INFINITY : __uint_as_float((uint32_t)(bin + 1 + kBinBias) << 16);
+    return bin == kBins - 1 ? INFINITY : __uint_as_float((uint32_t)(bin + 1 + kBinBias) << kBinShift);
   }
 
   // Zeroes the histogram; a barrier has to follow before the first add.
   QE_DEV void hist_clear() {
-    for (int i = threadIdx.x; i < 3 * kBins; i += kSampleThreads) (&sh.hist.piece[0][0])[i] = 0;
+    for (int i = threadIdx.x; i < 3 * kBins; i += kSampleThreads) (&sh.piece[0][0])[i] = 0;
   }
   QE_DEV void hist_add(int bin, u64 w) {
     const unsigned lo = (unsigned)w & 0xffffu, mid = (unsigned)(w >> 16) & 0xffffu, hi = (unsigned)(w >> 32);
-    if (lo) atomicAdd(&sh.hist.piece[0][bin], lo);
-    if (mid) atomicAdd(&sh.hist.piece[1][bin], mid);
-    if (hi) atomicAdd(&sh.hist.piece[2][bin], hi);
+    if (lo) atomicAdd(&sh.piece[0][bin], lo);
+    if (mid) atomicAdd(&sh.piece[1][bin], mid);
+    if (hi) atomicAdd(&sh.piece[2][bin], hi);
   }
   // The cluster's histogram, in slices: thread t of CTA r gets the sums of the bins
   // first_bin() ..., their running sum before them and the total.
@@ -254,9 +283,16 @@ struct Row {
   QE_DEV int slice() const { return kBins / size; }  // size is a power of two
   QE_DEV int per_slot() const { return slice() >= kSampleThreads ? slice() / kSampleThreads : 1; }
   QE_DEV Sums hist_sums() {
+    u64 put[kBins / kSampleThreads];
     __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += kSampleThreads)
-      sh.hist.sum[i] = (u64)sh.hist.piece[0][i] + ((u64)sh.hist.piece[1][i] << 16) + ((u64)sh.hist.piece[2][i] << 32);
+#pragma unroll
+    for (int j = 0; j < kBins / kSampleThreads; ++j) {
+      const int i = threadIdx.x + j * kSampleThreads;
+      put[j] = (u64)sh.piece[0][i] + ((u64)sh.piece[1][i] << 16) + ((u64)sh.piece[2][i] << 32);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kBins / kSampleThreads; ++j) sh.sum[threadIdx.x + j * kSampleThreads] = put[j];
     cluster_sync();  // every CTA's sums are there
     Sums s;
     const int m = per_slot();
@@ -270,7 +306,7 @@ struct Row {
         for (uint32_t r = 0; r < size; r += 4)
 #pragma unroll
           for (uint32_t k = 0; k < 4; ++k)
-            if (r + k < size) x[k] += ld_peer64(peer_addr(&sh.hist.sum[rank * slice() + i], r + k));
+            if (r + k < size) x[k] += ld_peer64(peer_addr(&sh.sum[rank * slice() + i], r + k));
         s.v[j] = (x[0] + x[1]) + (x[2] + x[3]);
       }
       sum += s.v[j];
@@ -294,9 +330,14 @@ struct Row {
     }
     return s;
   }
-  // The bin in which the sums, bin 0 first, reach `target` (1 <= target <= the
-  // total); above: the sum before it.  All CTAs get it.
-  QE_DEV int crossing(const Sums& s, u64 target, u64* above) {
+  // The bin in which the sums, bin 0 first, reach `target` (1 <= target; at most the
+  // total, the same in all CTAs, so that they agree whatever the logits are); above: the
+  // sum before it; in_bin: its own.  All CTAs get it.
+  QE_DEV int crossing(const Sums& s, u64 target, u64* above, u64* in_bin = nullptr) {
+    *above = 0;
+    if (in_bin) *in_bin = 0;
+    if (s.total == 0) return kBins - 1;
+    target = min(target, s.total);
     u64* out = sh.found[turn_found];
     turn_found ^= 1;
     u64 before = s.before;
@@ -306,11 +347,13 @@ struct Row {
         for (uint32_t r = 0; r < size; ++r) {
           st_peer64(peer_addr(out, r), (u64)(rank * slice() + threadIdx.x * per_slot() + j));
           st_peer64(peer_addr(out + 1, r), before);
+          st_peer64(peer_addr(out + 2, r), s.v[j]);
         }
       before += s.v[j];
     }
     cluster_sync();
     *above = out[1];
+    if (in_bin) *in_bin = out[2];
     return (int)out[0];
   }
 
@@ -360,42 +403,53 @@ struct Row {
 
   // Cuts the kept elements, in descending order, to the shortest run whose sum
   // of w reaches target (1 <= target <= their sum).  w is 0 for what is not kept.
-  template <typename F>
-  QE_DEV void cut_at(F w, int bin, u64 target) {
+  template <typename F, typename U>
+  QE_DEV void cut_at(F w, U unit, int bin, u64 target) {
     // bin: the coarse bin that the run ends in; target: what is to be reached within it.
+    // unit(x): what w is for a kept logit x.
     // Keys that the bin can hold: its bounds on x_max - x, widened by two
     // units in the last place of that difference
+    constexpr int KS = Elems<T>::kKeyShift;
     uint32_t k_hi = key_of(x_max), k_lo = key_of(-INFINITY);
-    const double d_lo = (double)__uint_as_float((uint32_t)(bin + kBinBias) << 16), d_hi = (double)bin_end(bin);
+    const double d_lo = (double)__uint_as_float((uint32_t)(bin + kBinBias) << kBinShift), d_hi = (double)bin_end(bin);
     if (bin > 0) k_hi = min(k_hi, key_of(__double2float_ru((double)x_max - d_lo * (1.0 - 2.4e-7))));
     if (bin < kBins - 1) k_lo = x_max < INFINITY ? key_of(__double2float_rd((double)x_max - d_hi * (1.0 + 2.4e-7))) : k_hi;
+    k_hi >>= KS;
+    k_lo >>= KS;
+    u64 in_bin;
     for (;;) {
       const uint32_t range = k_hi - k_lo;
       const int bits = 32 - __clz(range | 1);
-      const int sh_bits = bits > 10 ? bits - 10 : 0;
+      const int sh_bits = bits > kBinBits ? bits - kBinBits : 0;
       hist_clear();  // crossing() ends well after the last peer's read
       __syncthreads();
+      // (a key beyond an infinity's, from the missing bits, gives NaN: that infinity)
+      const float x_lo = fmaxf(logit_of(k_lo << KS), -INFINITY), x_hi = fminf(logit_of((k_hi << KS) | ((1u << KS) - 1)), INFINITY);
       each([&](float x, int i) {
-        const uint32_t k = key_of(x);
+        if (!(x >= x_lo && x <= x_hi)) return;  // the cheapest test first: few pass
+        const uint32_t k = key_of(x) >> KS;
         if (k < k_lo || k > k_hi || coarse_bin(x) != bin) return;
         const u64 v = w(x, i);
         if (v) hist_add((int)((k_hi - k) >> sh_bits), v);
       });
       u64 above;
       const Sums sums = hist_sums();
-      const int b = crossing(sums, target, &above);
+      const int b = crossing(sums, target, &above, &in_bin);
       target -= above;
       k_hi -= (uint32_t)b << sh_bits;
       if (sh_bits == 0) break;
       const uint32_t width = (1u << sh_bits) - 1;
       k_lo = k_hi - k_lo > width ? k_hi - width : k_lo;
     }
-    // of the elements with key k_hi, as many of the lowest indices as it takes
-    auto tie = [&](float x, int i) -> u64 { return key_of(x) == k_hi ? w(x, i) : 0; };
-    u64 mine, before;
-    const u64 all = running(tie, &mine, &before);
-    int at = thr == k_hi ? cut : 0x7fffffff;
-    if (all > target) {
+    k_hi = (k_hi << KS) | (k_hi >> (31 - KS) ? 0u : (1u << KS) - 1);  // a negative logit's key has ones there
+    // of the elements with this key, each of the same weight, as many of the lowest
+    // indices as it takes; all of them where one fewer would not reach the target
+    const float x_cut = logit_of(k_hi);
+    int at = thr == x_cut ? cut : 0x7fffffff;
+    if (in_bin - unit(x_cut) >= target) {
+      auto tie = [&](float x, int i) -> u64 { return x == x_cut ? w(x, i) : 0; };
+      u64 mine, before;
+      running(tie, &mine, &before);
       const int last = place_of(tie, mine, before, target - 1);  // the tie that reaches the target
       u64* out = sh.found[turn_found];
       turn_found ^= 1;
@@ -403,7 +457,7 @@ struct Row {
       cluster_sync();
       at = min(at, (int)out[0] + 1);
     }
-    thr = k_hi;
+    thr = x_cut;
     cut = at;
   }
 };
@@ -469,24 +523,29 @@ QE_DEV void finish_few(const Row<T>& r, int n, int top_k, bool cut_p, float top_
   auto logit = [&](u64 c) { return __uint_as_float((uint32_t)c); };
   u64 last = 0;  // the last kept candidate's {key, ~place}; all from it on are kept
   if (top_k > 0 || cut_p) {
-    // descending by key, ascending by place: a bitonic sort of the next power of two
-    int m = 32;
-    while (m < n) m *= 2;
-    for (int i = tid; i < m; i += kSampleThreads)
-      sh.few.order[i] = i < n ? ((u64)key_of(logit(sh.few.cand[i])) << 32) | (uint32_t)~i : 0;
-    __syncthreads();
-    for (int k = 2; k <= m; k *= 2)
-      for (int j = k / 2; j > 0; j /= 2) {
-        for (int i = tid; i < m / 2; i += kSampleThreads) {
-          const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
-          const u64 x = sh.few.order[lo], y = sh.few.order[hi];
-          if ((x < y) == ((lo & k) == 0)) {
-            sh.few.order[lo] = y;
-            sh.few.order[hi] = x;
+    // descending by key, ascending by place
+    auto item = [&](int i) -> u64 { return i < n ? ((u64)key_of(logit(sh.few.cand[i])) << 32) | (uint32_t)~i : 0; };
+    if (n <= kSampleThreads) {
+      const u64 x = block_sort<u64>(item(tid), sh.few.order);
+      __syncthreads();
+      sh.few.order[tid] = x;
+      __syncthreads();
+    } else {
+      for (int i = tid; i < kMaxCand; i += kSampleThreads) sh.few.order[i] = item(i);
+      __syncthreads();
+      for (int k = 2; k <= kMaxCand; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+          for (int i = tid; i < kMaxCand / 2; i += kSampleThreads) {
+            const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+            const u64 x = sh.few.order[lo], y = sh.few.order[hi];
+            if ((x < y) == ((lo & k) == 0)) {
+              sh.few.order[lo] = y;
+              sh.few.order[hi] = x;
+            }
           }
+          __syncthreads();
         }
-        __syncthreads();
-      }
+    }
     int keep = top_k > 0 && top_k < n ? top_k : n;
     if (cut_p) {
       u64 v[P], w[P], total;
@@ -539,7 +598,8 @@ __global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleA
   r.rank = a.cluster > 1 ? cluster_rank() : 0;
 
   cluster_arrive();  // waited for before the first access to a peer: it has to be running
-  if (threadIdx.x < kExpTable) sh.exp2_table[threadIdx.x] = exp2((double)threadIdx.x / kExpTable);
+  static_assert(kExpTable * kExpCopies == kSampleThreads, "one entry a thread");
+  sh.exp2_table[threadIdx.x / kExpCopies][threadIdx.x % kExpCopies] = exp2((double)(threadIdx.x / kExpCopies) / kExpTable);
   grid_dependency_wait();
   grid_launch_dependents();
 
@@ -583,7 +643,7 @@ __global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleA
   const u64* tops = r.all_gather(top);
   for (uint32_t k = 0; k < r.size; ++k) top = max(top, tops[k]);
   const uint32_t k_max = (uint32_t)top;
-  r.x_max = __uint_as_float(k_max & 0x80000000u ? k_max ^ 0x80000000u : ~k_max);
+  r.x_max = logit_of(k_max);
   if (r.x_max == -INFINITY) {  // nothing to choose from
     if (r.rank == 0 && threadIdx.x == 0) {
       a.token[row] = -1;
@@ -617,11 +677,16 @@ __global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleA
   int bin = kBins - 1;
   u64 target_p = 0, above = 0;
   if (cut_k) {
-    r.hist_clear();
+    // if each CTA has ceil(k / CTAs) threads whose largest logit is at least L, there are k such logits
+    const int j = (k + (int)r.size - 1) / (int)r.size;
+    const uint32_t sorted = block_sort<uint32_t>(key_of(best), reinterpret_cast<uint32_t*>(sh.few.order));
+    if ((int)threadIdx.x == min(j, kSampleThreads) - 1) sh.warp_sum[0] = j <= kSampleThreads ? sorted : 0;
     __syncthreads();
-    if (r.each_any()) atomicAdd(&sh.hist.piece[0][r.coarse_bin(best)], 1u);
-    const typename Row<T>::Sums sums = r.hist_sums();
-    if (sums.total >= (u64)k) far = Row<T>::bin_end(r.crossing(sums, (u64)k, &above));
+    const u64* bounds = r.all_gather(sh.warp_sum[0]);
+    uint32_t k_min = (uint32_t)bounds[0];
+    for (uint32_t c = 1; c < r.size; ++c) k_min = min(k_min, (uint32_t)bounds[c]);
+    // a lowest logit as a bound on the difference (which rounds the same way for both)
+    if (k_min > key_of(-INFINITY)) far = __uint_as_float(__float_as_uint(r.x_max - logit_of(k_min)) + 1);
   } else if (cut_p) {
     r.hist_clear();
     __syncthreads();
@@ -640,8 +705,10 @@ __global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleA
     const double d = -log(((double)least - 0.5) / (double)((u64)1 << a.shift)) * (double)t;
     far = fminf(far, __double2float_ru(d * (1.0 + 1e-6) + 1e-37));
   }
+  if (r.x_max == INFINITY) far = 0.f;  // only its equals, whose difference is no number
   if (far < INFINITY || a.V <= kMaxCand) {
-    auto near = [&](float x) { return r.x_max - x < far || x == r.x_max; };
+    const float same = r.x_max == INFINITY ? INFINITY : NAN;
+    auto near = [&](float x) { return r.x_max - x < far || x == same; };
     const u64 n = r.running([&](float x, int) -> u64 { return near(x) ? 1 : 0; }, &mine, &before);
     if (n <= kMaxCand) {
       // to the first CTA, in index order
@@ -658,15 +725,17 @@ __global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleA
   }
 
   if (cut_k) {
-    auto one = [&](float, int i) -> u64 { return i >= i0 && i < i1 ? 1 : 0; };
+    auto one = [](float x, int) -> u64 { return x > -INFINITY; };  // tokens that can be chosen (NaN cannot)
     r.hist_clear();
     __syncthreads();
     r.each([&](float x, int i) {
-      if (one(x, i)) atomicAdd(&sh.hist.piece[0][r.coarse_bin(x)], 1u);
+      if (one(x, i)) atomicAdd(&sh.piece[0][r.coarse_bin(x)], 1u);
     });
     const typename Row<T>::Sums sums = r.hist_sums();
-    bin = r.crossing(sums, (u64)k, &above);
-    r.cut_at(one, bin, (u64)k - above);
+    if (sums.total > (u64)k) {
+      bin = r.crossing(sums, (u64)k, &above);
+      r.cut_at(one, [](float) -> u64 { return 1; }, bin, (u64)k - above);
+    }
   }
   auto mass = [&](float x, int i) -> u64 { return r.kept(x, i) ? r.weight(x) : 0; };
   if (cut_p) {
@@ -681,7 +750,7 @@ __global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleA
       target_p = mass_target(tp, sums.total);
       bin = r.crossing(sums, target_p, &above);
     }
-    r.cut_at(mass, bin, target_p - above);
+    r.cut_at(mass, [&](float x) { return r.weight(x); }, bin, target_p - above);
   }
   auto final_mass = [&](float x, int i) -> u64 {
     const u64 w = mass(x, i);
@@ -699,12 +768,13 @@ __global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleA
 
 template <typename T>
 cudaError_t launch_sample_t(SampleArgs a, cudaStream_t s) {
-  // CTAs per row: enough that a CTA's run is short (few rows: latency) or that several
-  // CTAs share a multiprocessor's memory (many rows)
+  // CTAs per row: so many that two CTAs (what the registers allow) fit into a
+  // multiprocessor's memory, and more where that still leaves all of them running at once
   const int es = (int)sizeof(T);
+  const int at_once = 2 * dev_info().sms;
   int cl = 1;
-  while (cl < 8 && (long long)a.V * es / cl > 32768) cl *= 2;
-  if ((long long)a.V * es / cl > 56 * 1024) cl = 16;
+  while (cl < 16 && (long long)a.V * es / cl > 80 * 1024) cl *= 2;
+  while (cl < 16 && (long long)a.V * es / cl > 8 * 1024 && (long long)a.B * cl * 2 <= at_once) cl *= 2;
   a.cluster = cl;
   const int n = 16 / es;
   a.run = ((a.V + cl - 1) / cl + n - 1) / n * n;
