@@ -14,17 +14,23 @@
 // The rounding moves a border by at most V 2^-(S+1) of the largest weight; a
 // weight below 2^-(S+1) of it counts as 0.
 //
-// The row is read once.  A cluster of CTAs shares it, each holding a run of the
-// row as stored in its shared memory; a thread owns an odd number of
+// A cluster of CTAs shares a row.  Few rows: each CTA holds its run of the row as stored in its
+// shared memory, so that the row is read once; a thread owns an odd number of
 // consecutive 16-byte pieces, so that threads are in index order (which the
-// running sums need) and their 16-byte reads fall on different banks.
+// running sums need) and their 16-byte reads fall on different banks.  Many rows
+// (STREAM): the shared memory would leave few rows at work at a time (18 of 800 KB),
+// so that four CTAs a row read it from global memory, mostly the L2 cache, in
+// every pass, each warp a run of its own, and 74 rows are at work.  Measured at 256 rows of
+// 200000 fp32 logits: 443 us from shared memory (16 CTAs a row), streamed by 1, 2, 4
+// and 8 CTAs a row 388, 268, 250 and 301 us; at 64 rows of 100003 bf16 logits 64 us and
+// (by 4) 85 us.
 //
 // What costs time is the weights (a dozen fp64 operations each) and the
 // cluster's barriers, so both are avoided:
 //   - candidates: a bound on x_max - x that holds for every token that can be
 //     kept comes from min_p, from a histogram of the threads' largest logits (the
 //     k-th largest of them is at most the k-th largest logit), or from a histogram
-//     of the weights over x_max - x.  Up to 1024 candidates are gathered, in index
+//     of the weights over x_max - x.  Up to 2048 candidates are gathered, in index
 //     order, by the first CTA, which sorts them and finishes alone;
 //   - otherwise the cut is found without a sort: the histogram (2048 bins, 8
 //     mantissa bits of 8 binades), summed over the cluster through distributed
@@ -54,7 +60,10 @@ constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kBinBits = 11, kBins = 1 << kBinBits;
 constexpr int kBinShift = 15;                // 8 mantissa bits of x_max - x
 constexpr int kBinBias = (127 - 3) << 8;  // bin 0: below 2^-3 (1 + 2^-8); the last: from 2^5 on
-constexpr int kMaxCand = 1024;
+constexpr int kMaxCand = 2048;
+constexpr int kStreamCluster = 4;
+constexpr int kAhead = 2;   // STREAM: 16-byte pieces a thread has on their way
+constexpr int kGroups = 4;  // groups of a thread's logits of which the largest is kept
 constexpr int kMaxVocab = 1 << 19;
 constexpr int kMaxCluster = 16;
 
@@ -194,13 +203,15 @@ QE_DEV V block_sort(V v, V* buf) {
   return v;
 }
 
-template <typename T>
+template <typename T, bool STREAM>
 struct Row {
   static constexpr int N = Elems<T>::N;
   const SampleArgs& a;
   SampleShared& sh;
   const uint4* data;   // the run as stored; its first piece holds element `first` at 0
-  int pieces, per_thread;
+  int pieces, per;     // pieces of the run, and of a thread (STREAM: of a warp)
+  u64 cta_before = 0, cta_sum = 0;  // of the CTA, as running() last found it
+  int lo, hi;          // STREAM: elements [lo, hi) from `first` are the row's
   int first;           // index in the row of element 0 of piece 0 (may be below the run's start)
   uint32_t rank, size;
   int turn = 0, turn_found = 0;
@@ -211,24 +222,82 @@ struct Row {
 
   QE_DEV Row(const SampleArgs& a_, SampleShared& s_) : a(a_), sh(s_) {}
 
-  // f(x, index) over this thread's elements, in index order
+  // Piece p of the row in global memory; what is not the row's counts as -inf.
+  QE_DEV uint4 piece_at(int p) const {
+    if (p * N >= lo && (p + 1) * N <= hi) return __ldg(data + p);
+    uint4 w;
+    T* t = reinterpret_cast<T*>(&w);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int i = p * N + e;
+      t[e] = i >= lo && i < hi ? reinterpret_cast<const T*>(data)[i] : Elems<T>::lowest();
+    }
+    return w;
+  }
+  QE_DEV float element(int i) const { return (float)reinterpret_cast<const T*>(data)[i - first]; }  // of index i
+
+  // f(x, index) over this thread's elements: consecutive ones in index order; STREAM: every
+  // 32nd piece of the warp's run
   template <typename F>
   QE_DEV void each(F f) const {
-    const int p0 = threadIdx.x * per_thread, p1 = min(pieces, p0 + per_thread);
-    for (int p = p0; p < p1; ++p) {
-      float x[N];
-      Elems<T>::get(data[p], x);
+    if constexpr (STREAM) {
+      const int p0 = (threadIdx.x >> 5) * per, p1 = min(pieces, p0 + per);
+      // The row's first and last piece may be partial: the lanes that have them take them
+      // by elements, so that the loop's loads are plain ones, kAhead pieces on their way
+      // while as many are worked on.
+      const int lane = threadIdx.x & 31, head = lo > 0, tail = hi < pieces * N;
+#pragma unroll 1
+      for (int side = 0; side < 2; ++side) {
+        const int p = side ? pieces - 1 : 0;
+        if (!(side ? tail && (pieces > 1 || !head) : head) || p < p0 || p >= p1 || lane != 0) continue;
+#pragma unroll 1
+        for (int i = max(lo, p * N); i < min(hi, (p + 1) * N); ++i) f(element(first + i), first + i);
+      }
+      const int end = min(p1, pieces - tail);
+      int p = max(p0, head) + lane;
+      uint4 q[kAhead];
 #pragma unroll
-      for (int e = 0; e < N; ++e) f(x[e], first + p * N + e);
+      for (int u = 0; u < kAhead; ++u)
+        if (p + 32 * u < end) q[u] = __ldg(data + p + 32 * u);
+#pragma unroll 1
+      for (; p < end; p += 32 * kAhead) {
+        uint4 n[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (p + 32 * (kAhead + u) < end) n[u] = __ldg(data + p + 32 * (kAhead + u));
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (p + 32 * u < end) {
+            float x[N];
+            Elems<T>::get(q[u], x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) f(x[e], first + (p + 32 * u) * N + e);
+          }
+          q[u] = n[u];
+        }
+      }
+    } else {
+      const int p0 = threadIdx.x * per, p1 = min(pieces, p0 + per);
+      for (int p = p0; p < p1; ++p) {
+        float x[N];
+        Elems<T>::get(data[p], x);
+#pragma unroll
+        for (int e = 0; e < N; ++e) f(x[e], first + p * N + e);
+      }
     }
   }
 
+  // All CTAs of the row, with what they wrote to each other.
+  QE_DEV void sync_all() const {
+    if (STREAM && size == 1) __syncthreads();
+    else cluster_sync();
+  }
   // Every CTA's v, by rank, in the returned array (valid until the next but one call).
   QE_DEV const u64* all_gather(u64 v) {
     u64* slots = sh.xch[turn];
     turn ^= 1;
     if (threadIdx.x < size) st_peer64(peer_addr(slots + rank, threadIdx.x), v);
-    cluster_sync();
+    sync_all();
     return slots;
   }
   // Weight of a logit as a multiple of 2^-S: e^y = 2^(k / 32) e^r with k the whole
@@ -237,8 +306,10 @@ struct Row {
   // is below 2^52, so adding 2^52 rounds it to a whole number in the low bits.  No
   // branch: the elements of a piece are worked on side by side.  Below -45 (2^-64), and
   // for -inf and NaN, whatever comes out is dropped.
+  // INF: the row's largest logit is +inf, and only its equals weigh.
+  template <bool INF>
   QE_DEV u64 weight(float x) const {
-    if (x_max == INFINITY) return x == x_max ? (u64)1 << a.shift : 0;  // the same for the whole row
+    if constexpr (INF) return x == INFINITY ? (u64)1 << a.shift : 0;
     const double y = ((double)x - (double)x_max) * inv_t;
     const double km = fma(y, 46.166241308446828, 6755399441055744.0);
     const double r = fma(6755399441055744.0 - km, 0.021660849392498291, y);
@@ -253,7 +324,7 @@ struct Row {
     const u64 w = (u64)__double_as_longlong(fma(p, two, 4503599627370496.0)) & 0xfffffffffffffull;
     return y > -45.0 ? w : 0;
   }
-  QE_DEV bool kept(float x, int i) const { return x > thr || (x == thr && i < cut); }
+  QE_DEV bool kept(float x, int i) const { return x > thr || (x == thr && i < cut); }  // thr -inf: all
 
   QE_DEV int coarse_bin(float x) const {
     if (!(x < x_max)) return x == x_max ? 0 : kBins - 1;
@@ -293,7 +364,7 @@ struct Row {
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kBins / kSampleThreads; ++j) sh.sum[threadIdx.x + j * kSampleThreads] = put[j];
-    cluster_sync();  // every CTA's sums are there
+    sync_all();  // every CTA's sums are there
     Sums s;
     const int m = per_slot();
     u64 sum = 0;
@@ -351,13 +422,14 @@ struct Row {
         }
       before += s.v[j];
     }
-    cluster_sync();
+    sync_all();
     *above = out[1];
     if (in_bin) *in_bin = out[2];
     return (int)out[0];
   }
 
-  // Sum of w over the row; mine, before: this thread's part and what comes before it.
+  // Sum of w over the row; mine, before: this thread's (STREAM: warp's) part and what
+  // comes before it.
   template <typename F>
   QE_DEV u64 running(F w, u64* mine, u64* before) {
     u64 m = 0;
@@ -366,6 +438,7 @@ struct Row {
     __syncthreads();
     if ((threadIdx.x & 31) == 31) sh.warp_sum[threadIdx.x >> 5] = scan;
     __syncthreads();
+    if constexpr (STREAM) scan = m = sh.warp_sum[threadIdx.x >> 5];
     u64 all = 0;
 #pragma unroll
     for (int k = 0; k < kSampleWarps; ++k) {
@@ -373,32 +446,129 @@ struct Row {
       all += sh.warp_sum[k];
     }
     const u64* runs = all_gather(all);
-    u64 b = scan - m, total = 0;
+    u64 total = 0;
+    cta_before = 0;
+    cta_sum = all;
     for (uint32_t r = 0; r < size; ++r) {
-      if (r < rank) b += runs[r];
+      if (r < rank) cta_before += runs[r];
       total += runs[r];
     }
     *mine = m;
-    *before = b;
+    *before = cta_before + scan - m;
     return total;
   }
-  // In the warp in one of whose threads' parts the running sum exceeds `target` (below
-  // the total): the first such index; -1 in the others.  The warp shares that part out.
+  // In the warp in whose part the running sum exceeds `target` (below the total): the
+  // first such index; -1 in the others.  All threads call it, with what running() gave.
+  // The part is shared out: among the lanes (STREAM: among all warps, then the lanes).
   template <typename F>
-  QE_DEV int place_of(F w, u64 mine, u64 before, u64 target) const {
-    const unsigned owner = __ballot_sync(0xffffffffu, before <= target && target < before + mine);
-    if (!owner) return -1;
-    const int src = __ffs(owner) - 1, lane = threadIdx.x & 31, p0 = ((threadIdx.x & ~31) + src) * per_thread;
-    const int end = min(pieces, p0 + per_thread) * N;
-    u64 base = __shfl_sync(0xffffffffu, before, src);
-    for (int e0 = p0 * N; e0 < end; e0 += 32) {
-      const int e = e0 + lane;
-      const u64 scan = base + warp_scan(e < end ? w((float)reinterpret_cast<const T*>(data)[e], first + e) : 0);
-      const unsigned past = __ballot_sync(0xffffffffu, scan > target);
-      if (past) return first + e0 + __ffs(past) - 1;
-      base = __shfl_sync(0xffffffffu, scan, 31);
+  QE_DEV int place_of(F w, u64 mine, u64 before, u64 target) {
+    const int lane = threadIdx.x & 31;
+    bool here = before <= target && target < before + mine;
+    if constexpr (STREAM) {
+      const int warp = threadIdx.x >> 5;
+      u64* at = sh.found[turn_found];
+      turn_found ^= 1;
+      if (!(cta_before <= target && target < cta_before + cta_sum)) return -1;  // not in this CTA
+      if (here && lane == 0) {
+        at[0] = (u64)warp;
+        at[1] = before;
+      }
+      __syncthreads();
+      const int s0 = (int)at[0] * per, s1 = min(pieces, s0 + per), part = (s1 - s0 + kSampleWarps - 1) / kSampleWarps;
+      const int p0 = min(s1, s0 + warp * part), p1 = min(s1, p0 + part);
+      auto piece_sum = [&](int p) {
+        float x[N];
+        Elems<T>::get(piece_at(p), x);
+        u64 m = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) m += w(x[e], first + p * N + e);
+        return m;
+      };
+      u64 m = 0;
+      for (int p = p0 + lane; p < p1; p += 32) m += piece_sum(p);
+      m = warp_scan(m);
+      if (lane == 31) sh.warp_sum[warp] = m;
+      __syncthreads();
+      u64 base = at[1];
+      for (int k = 0; k < warp; ++k) base += sh.warp_sum[k];
+      if (!(base <= target && target < base + sh.warp_sum[warp])) return -1;
+      for (int p = p0; p < p1; p += 32) {
+        const u64 own = p + lane < p1 ? piece_sum(p + lane) : 0, scan = base + warp_scan(own);
+        const unsigned past = __ballot_sync(0xffffffffu, scan > target);
+        if (past) {
+          const int src = __ffs(past) - 1;
+          int found = -1;
+          if (lane == src) {
+            u64 sum = scan - own;
+            float x[N];
+            Elems<T>::get(piece_at(p + lane), x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              sum += w(x[e], first + (p + lane) * N + e);
+              if (found < 0 && sum > target) found = first + (p + lane) * N + e;
+            }
+          }
+          return __shfl_sync(0xffffffffu, found, src);
+        }
+        base = __shfl_sync(0xffffffffu, scan, 31);
+      }
+      return -1;
+    } else {
+      const unsigned owner = __ballot_sync(0xffffffffu, here);
+      if (!owner) return -1;
+      const int src = __ffs(owner) - 1, p0 = ((threadIdx.x & ~31) + src) * per;
+      const int end = min(pieces, p0 + per) * N;
+      u64 base = __shfl_sync(0xffffffffu, before, src);
+      for (int e0 = p0 * N; e0 < end; e0 += 32) {
+        const int e = e0 + lane;
+        const u64 scan = base + warp_scan(e < end ? w(element(first + e), first + e) : 0);
+        const unsigned past = __ballot_sync(0xffffffffu, scan > target);
+        if (past) return first + e0 + __ffs(past) - 1;
+        base = __shfl_sync(0xffffffffu, scan, 31);
+      }
+      return -1;
     }
-    return -1;
+  }
+  // {index, logit} of the elements that f(x) picks, in index order, to the first CTA's
+  // list; before: as running() counted them.
+  template <typename F>
+  QE_DEV void gather(F f, u64 before) const {
+    uint32_t to = peer_addr(sh.few.cand, 0) + (uint32_t)before * 8;
+    if constexpr (STREAM) {
+      const int lane = threadIdx.x & 31, p0 = (threadIdx.x >> 5) * per, p1 = min(pieces, p0 + per);
+      for (int p = p0; p < p1; p += 32) {
+        float x[N];
+        int n = 0;
+        if (p + lane < p1) {
+          Elems<T>::get(piece_at(p + lane), x);
+#pragma unroll
+          for (int e = 0; e < N; ++e) n += f(x[e]);
+        }
+        if (!__any_sync(0xffffffffu, n)) continue;
+        int scan = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, scan, d);
+          if (lane >= d) scan += o;
+        }
+        uint32_t at = to + (scan - n) * 8;
+        if (n) {
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (f(x[e])) {
+              st_peer64(at, ((u64)(uint32_t)(first + (p + lane) * N + e) << 32) | __float_as_uint(x[e]));
+              at += 8;
+            }
+        }
+        to += __shfl_sync(0xffffffffu, scan, 31) * 8;
+      }
+    } else {
+      each([&](float x, int i) {
+        if (!f(x)) return;
+        st_peer64(to, ((u64)(uint32_t)i << 32) | __float_as_uint(x));
+        to += 8;
+      });
+    }
   }
 
   // Cuts the kept elements, in descending order, to the shortest run whose sum
@@ -454,7 +624,7 @@ struct Row {
       u64* out = sh.found[turn_found];
       turn_found ^= 1;
       if (last >= 0 && (threadIdx.x & 31) < size) st_peer64(peer_addr(out, threadIdx.x & 31), (u64)last);
-      cluster_sync();
+      sync_all();
       at = min(at, (int)out[0] + 1);
     }
     thr = x_cut;
@@ -496,8 +666,8 @@ QE_DEV u64 choice_target(float u, u64 total) {
 
 // The cuts and the choice among n <= kMaxCand candidates in index order, by one CTA.
 // target_p: the mass that top_p keeps, where that is known already (no top_k).
-template <typename T>
-QE_DEV void finish_few(const Row<T>& r, int n, int top_k, bool cut_p, float top_p, u64 target_p, u64 least, float u, int row) {
+template <bool INF, typename T, bool STREAM>
+QE_DEV void finish_few(const Row<T, STREAM>& r, int n, int top_k, bool cut_p, float top_p, u64 target_p, u64 least, float u, int row) {
   SampleShared& sh = r.sh;
   const SampleArgs& a = r.a;
   constexpr int P = kMaxCand / kSampleThreads;  // places per thread
@@ -552,7 +722,7 @@ QE_DEV void finish_few(const Row<T>& r, int n, int top_k, bool cut_p, float top_
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         const int i = P * tid + j;
-        w[j] = v[j] = i < keep ? r.weight(logit(sh.few.cand[(uint32_t)~sh.few.order[i]])) : 0;
+        w[j] = v[j] = i < keep ? r.template weight<INF>(logit(sh.few.cand[(uint32_t)~sh.few.order[i]])) : 0;
       }
       block_running(v, &total);
       const u64 target = top_k > 0 ? mass_target(top_p, total) : target_p;
@@ -572,7 +742,7 @@ QE_DEV void finish_few(const Row<T>& r, int n, int top_k, bool cut_p, float top_
     u64 x = 0;
     if (i < n) {
       const float l = logit(sh.few.cand[i]);
-      if ((((u64)key_of(l) << 32) | (uint32_t)~i) >= last) x = r.weight(l);
+      if ((((u64)key_of(l) << 32) | (uint32_t)~i) >= last) x = r.template weight<INF>(l);
       if (x < least) x = 0;
     }
     w[j] = v[j] = x;
@@ -587,15 +757,131 @@ QE_DEV void finish_few(const Row<T>& r, int n, int top_k, bool cut_p, float top_
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleArgs a) {
+// The cuts and the choice, once the row's largest logit is known.
+template <bool INF, typename T, bool STREAM>
+QE_DEV void choose(Row<T, STREAM>& r, float best, const float (&group)[kGroups], float t, int k, float tp, float mp, float u,
+                   int row) {
+  using R = Row<T, STREAM>;
+  SampleShared& sh = r.sh;
+  const SampleArgs& a = r.a;
+  u64 mine, before;
+  u64 least = 1;  // of a kept weight
+  if (mp > 0.f) least = max((u64)1, (u64)ceil((double)fminf(mp, 1.f) * (double)((u64)1 << a.shift)));
+  const bool cut_k = k > 0 && k < a.V, cut_p = tp < 1.f;
+
+  // A bound on x_max - x for the candidates, all tokens that can be kept
+  float far = INFINITY;
+  int bin = kBins - 1;
+  u64 target_p = 0, above = 0;
+  if (cut_k) {
+    // the k-th largest of the largest logits of disjoint groups is at most the k-th largest logit
+    if constexpr (STREAM) {
+      r.hist_clear();
+      __syncthreads();
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+        if (group[g] > -INFINITY) atomicAdd(&sh.piece[0][r.coarse_bin(group[g])], 1u);
+      const typename R::Sums sums = r.hist_sums();
+      if (sums.total >= (u64)k) far = R::bin_end(r.crossing(sums, (u64)k, &above));
+    } else {
+      // if each CTA has ceil(k / CTAs) threads whose largest logit is at least L, there are k such logits
+      const int j = (k + (int)r.size - 1) / (int)r.size;
+      const uint32_t sorted = block_sort<uint32_t>(key_of(best), reinterpret_cast<uint32_t*>(sh.few.order));
+      if ((int)threadIdx.x == min(j, kSampleThreads) - 1) sh.warp_sum[0] = j <= kSampleThreads ? sorted : 0;
+      __syncthreads();
+      const u64* bounds = r.all_gather(sh.warp_sum[0]);
+      uint32_t k_min = (uint32_t)bounds[0];
+      for (uint32_t c = 1; c < r.size; ++c) k_min = min(k_min, (uint32_t)bounds[c]);
+      // a lowest logit as a bound on the difference (which rounds the same way for both)
+      if (k_min > key_of(-INFINITY)) far = __uint_as_float(__float_as_uint(r.x_max - logit_of(k_min)) + 1);
+    }
+  } else if (cut_p) {
+    r.hist_clear();
+    __syncthreads();
+    r.each([&](float x, int) {
+      const u64 w = r.template weight<INF>(x);
+      if (w) r.hist_add(r.coarse_bin(x), w);
+    });
+    const typename R::Sums sums = r.hist_sums();
+    target_p = mass_target(tp, sums.total);
+    bin = r.crossing(sums, target_p, &above);
+    far = R::bin_end(bin);
+  }
+  // (with a top_k, top_p goes by the mass of all its tokens)
+  if (mp > 0.f && !(cut_k && cut_p)) {
+    // a kept weight is at least least - 1/2 before its rounding; 1e-6 covers the rounding of x_max - x
+    const double d = -log(((double)least - 0.5) / (double)((u64)1 << a.shift)) * (double)t;
+    far = fminf(far, __double2float_ru(d * (1.0 + 1e-6) + 1e-37));
+  }
+  if (INF) far = 0.f;  // only its equals, whose difference is no number
+  if (far < INFINITY || a.V <= kMaxCand) {
+    auto near = [&](float x) { return INF ? x == INFINITY : r.x_max - x < far; };
+    const u64 n = r.running([&](float x, int) -> u64 { return near(x) ? 1 : 0; }, &mine, &before);
+    if (n <= kMaxCand) {
+      r.gather(near, before);
+      r.sync_all();
+      if (r.rank == 0) finish_few<INF>(r, (int)n, cut_k ? k : 0, cut_p, tp, target_p, least, u, row);
+      return;
+    }
+  }
+
+  if (cut_k) {
+    auto one = [](float x, int) -> u64 { return x > -INFINITY; };  // tokens that can be chosen (NaN cannot)
+    r.hist_clear();
+    __syncthreads();
+    r.each([&](float x, int i) {
+      if (one(x, i)) atomicAdd(&sh.piece[0][r.coarse_bin(x)], 1u);
+    });
+    const typename R::Sums sums = r.hist_sums();
+    if (sums.total > (u64)k) {
+      bin = r.crossing(sums, (u64)k, &above);
+      r.cut_at(one, [](float) -> u64 { return 1; }, bin, (u64)k - above);
+    }
+  }
+  auto mass = [&](float x, int i) -> u64 { return r.kept(x, i) ? r.template weight<INF>(x) : 0; };
+  if (cut_p) {
+    if (cut_k) {
+      r.hist_clear();
+      __syncthreads();
+      r.each([&](float x, int i) {
+        const u64 w = mass(x, i);
+        if (w) r.hist_add(r.coarse_bin(x), w);
+      });
+      const typename R::Sums sums = r.hist_sums();
+      target_p = mass_target(tp, sums.total);
+      bin = r.crossing(sums, target_p, &above);
+    }
+    r.cut_at(mass, [&](float x) { return r.template weight<INF>(x); }, bin, target_p - above);
+  }
+  auto pick = [&](auto w) {
+    const u64 total = r.running(w, &mine, &before);
+    const int at = r.place_of(w, mine, before, choice_target(u, total));
+    if (at >= 0 && (threadIdx.x & 31) == 0) {
+      a.token[row] = at;
+      if (a.logprob) a.logprob[row] = (float)log((double)r.template weight<INF>(r.element(at)) / (double)total);
+    }
+  };
+  // (nothing cut: no test for each logit)
+  if (!cut_k && !cut_p && least == 1)
+    pick([&](float x, int) { return r.template weight<INF>(x); });
+  else
+    pick([&](float x, int i) -> u64 {
+      const u64 w = mass(x, i);
+      return w >= least ? w : 0;
+    });
+  r.sync_all();
+}
+
+template <typename T, bool STREAM>
+__global__ void __launch_bounds__(kSampleThreads, 2) qe_sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int N = Elems<T>::N;
   SampleShared& sh = *reinterpret_cast<SampleShared*>(smem + a.smem_row);
   const int row = blockIdx.x / a.cluster;
-  Row<T> r(a, sh);
+  using R = Row<T, STREAM>;
+  R r(a, sh);
   r.size = a.cluster;
-  r.rank = a.cluster > 1 ? cluster_rank() : 0;
+  r.rank = a.cluster == 1 ? 0 : cluster_rank();
 
   cluster_arrive();  // waited for before the first access to a peer: it has to be running
   static_assert(kExpTable * kExpCopies == kSampleThreads, "one entry a thread");
@@ -613,25 +899,46 @@ __global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleA
     const int n = i1 - i0;
     r.first = i0 - skew;
     r.pieces = n > 0 ? (skew + n + N - 1) / N : 0;
-    r.per_thread = ((r.pieces + kSampleThreads - 1) / kSampleThreads) | 1;
-    r.data = reinterpret_cast<const uint4*>(smem);
-    T* dst = reinterpret_cast<T*>(smem);
     const T* src = p0 - skew;
-    for (int p = threadIdx.x; p < r.pieces; p += kSampleThreads) {
-      if (p * N >= skew && (p + 1) * N <= skew + n) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst + p * N)), "l"(src + p * N) : "memory");
-      } else {
-        for (int e = p * N; e < (p + 1) * N; ++e)
-          dst[e] = e >= skew && e < skew + n ? src[e] : Elems<T>::lowest();
+    if constexpr (STREAM) {
+      r.data = reinterpret_cast<const uint4*>(src);
+      r.lo = skew;
+      r.hi = skew + n;
+      r.per = ((r.pieces + kSampleWarps - 1) / kSampleWarps + 31) & ~31;
+      __syncthreads();
+    } else {
+      r.per = ((r.pieces + kSampleThreads - 1) / kSampleThreads) | 1;
+      r.data = reinterpret_cast<const uint4*>(smem);
+      T* dst = reinterpret_cast<T*>(smem);
+      for (int p = threadIdx.x; p < r.pieces; p += kSampleThreads) {
+        if (p * N >= skew && (p + 1) * N <= skew + n) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst + p * N)), "l"(src + p * N) : "memory");
+        } else {
+          for (int e = p * N; e < (p + 1) * N; ++e)
+            dst[e] = e >= skew && e < skew + n ? src[e] : Elems<T>::lowest();
+        }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
   }
 
   // the largest logit
-  float best = -INFINITY;
-  r.each([&](float x, int) { best = fmaxf(best, x); });  // NaN loses
+  float best = -INFINITY, group[kGroups];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) group[g] = -INFINITY;
+  if constexpr (STREAM) {
+    r.each([&](float x, int i) {
+      const int g = (i - r.first) & (kGroups - 1);  // known when the code is compiled
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k)
+        if (g == k) group[k] = fmaxf(group[k], x);
+    });
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) best = fmaxf(best, group[g]);
+  } else {
+    r.each([&](float x, int) { best = fmaxf(best, x); });  // NaN loses
+  }
   u64 top = key_of(best);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -649,7 +956,7 @@ __global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleA
       a.token[row] = -1;
       if (a.logprob) a.logprob[row] = -INFINITY;
     }
-    cluster_sync();
+    r.sync_all();
     return;
   }
   const float t = a.temperature ? a.temperature[row] : 1.f;
@@ -664,106 +971,43 @@ __global__ void __launch_bounds__(kSampleThreads) qe_sample_kernel(const SampleA
       a.token[row] = at;
       if (a.logprob) a.logprob[row] = 0.f;
     }
-    cluster_sync();
+    r.sync_all();
     return;
   }
   r.inv_t = 1.0 / (double)t;
-  u64 least = 1;  // of a kept weight
-  if (mp > 0.f) least = max((u64)1, (u64)ceil((double)fminf(mp, 1.f) * (double)((u64)1 << a.shift)));
-  const bool cut_k = k > 0 && k < a.V, cut_p = tp < 1.f;
+  if (r.x_max == INFINITY) choose<true>(r, best, group, t, k, tp, mp, u, row);
+  else choose<false>(r, best, group, t, k, tp, mp, u, row);
+}
 
-  // A bound on x_max - x for the candidates, all tokens that can be kept
-  float far = INFINITY;
-  int bin = kBins - 1;
-  u64 target_p = 0, above = 0;
-  if (cut_k) {
-    // if each CTA has ceil(k / CTAs) threads whose largest logit is at least L, there are k such logits
-    const int j = (k + (int)r.size - 1) / (int)r.size;
-    const uint32_t sorted = block_sort<uint32_t>(key_of(best), reinterpret_cast<uint32_t*>(sh.few.order));
-    if ((int)threadIdx.x == min(j, kSampleThreads) - 1) sh.warp_sum[0] = j <= kSampleThreads ? sorted : 0;
-    __syncthreads();
-    const u64* bounds = r.all_gather(sh.warp_sum[0]);
-    uint32_t k_min = (uint32_t)bounds[0];
-    for (uint32_t c = 1; c < r.size; ++c) k_min = min(k_min, (uint32_t)bounds[c]);
-    // a lowest logit as a bound on the difference (which rounds the same way for both)
-    if (k_min > key_of(-INFINITY)) far = __uint_as_float(__float_as_uint(r.x_max - logit_of(k_min)) + 1);
-  } else if (cut_p) {
-    r.hist_clear();
-    __syncthreads();
-    r.each([&](float x, int) {
-      const u64 w = r.weight(x);
-      if (w) r.hist_add(r.coarse_bin(x), w);
-    });
-    const typename Row<T>::Sums sums = r.hist_sums();
-    target_p = mass_target(tp, sums.total);
-    bin = r.crossing(sums, target_p, &above);
-    far = Row<T>::bin_end(bin);
+template <typename T, bool STREAM>
+cudaError_t launch_sample_as(const SampleArgs& a, cudaStream_t s) {
+  static std::atomic<bool> set[64];  // per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!set[dev]) {
+    e = cudaFuncSetAttribute(qe_sample_kernel<T, STREAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(qe_sample_kernel<T, STREAM>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    set[dev] = true;
   }
-  // (with a top_k, top_p goes by the mass of all its tokens)
-  if (mp > 0.f && !(cut_k && cut_p)) {
-    // a kept weight is at least least - 1/2 before its rounding; 1e-6 covers the rounding of x_max - x
-    const double d = -log(((double)least - 0.5) / (double)((u64)1 << a.shift)) * (double)t;
-    far = fminf(far, __double2float_ru(d * (1.0 + 1e-6) + 1e-37));
-  }
-  if (r.x_max == INFINITY) far = 0.f;  // only its equals, whose difference is no number
-  if (far < INFINITY || a.V <= kMaxCand) {
-    const float same = r.x_max == INFINITY ? INFINITY : NAN;
-    auto near = [&](float x) { return r.x_max - x < far || x == same; };
-    const u64 n = r.running([&](float x, int) -> u64 { return near(x) ? 1 : 0; }, &mine, &before);
-    if (n <= kMaxCand) {
-      // to the first CTA, in index order
-      uint32_t to = peer_addr(sh.few.cand, 0) + (uint32_t)before * 8;
-      r.each([&](float x, int i) {
-        if (!near(x)) return;
-        st_peer64(to, ((u64)(uint32_t)i << 32) | __float_as_uint(x));
-        to += 8;
-      });
-      cluster_sync();
-      if (r.rank == 0) finish_few(r, (int)n, cut_k ? k : 0, cut_p, tp, target_p, least, u, row);
-      return;
-    }
-  }
-
-  if (cut_k) {
-    auto one = [](float x, int) -> u64 { return x > -INFINITY; };  // tokens that can be chosen (NaN cannot)
-    r.hist_clear();
-    __syncthreads();
-    r.each([&](float x, int i) {
-      if (one(x, i)) atomicAdd(&sh.piece[0][r.coarse_bin(x)], 1u);
-    });
-    const typename Row<T>::Sums sums = r.hist_sums();
-    if (sums.total > (u64)k) {
-      bin = r.crossing(sums, (u64)k, &above);
-      r.cut_at(one, [](float) -> u64 { return 1; }, bin, (u64)k - above);
-    }
-  }
-  auto mass = [&](float x, int i) -> u64 { return r.kept(x, i) ? r.weight(x) : 0; };
-  if (cut_p) {
-    if (cut_k) {
-      r.hist_clear();
-      __syncthreads();
-      r.each([&](float x, int i) {
-        const u64 w = mass(x, i);
-        if (w) r.hist_add(r.coarse_bin(x), w);
-      });
-      const typename Row<T>::Sums sums = r.hist_sums();
-      target_p = mass_target(tp, sums.total);
-      bin = r.crossing(sums, target_p, &above);
-    }
-    r.cut_at(mass, [&](float x) { return r.weight(x); }, bin, target_p - above);
-  }
-  auto final_mass = [&](float x, int i) -> u64 {
-    const u64 w = mass(x, i);
-    return w >= least ? w : 0;
-  };
-  const u64 total = r.running(final_mass, &mine, &before);
-  const int at = r.place_of(final_mass, mine, before, choice_target(u, total));
-  if (at >= 0 && (threadIdx.x & 31) == 0) {
-    a.token[row] = at;
-    const float x = (float)reinterpret_cast<const T*>(smem)[at - r.first];
-    if (a.logprob) a.logprob[row] = (float)log((double)r.weight(x) / (double)total);
-  }
-  cluster_sync();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.B * a.cluster));
+  cfg.blockDim = dim3(kSampleThreads);
+  cfg.dynamicSmemBytes = a.smem_row + sizeof(SampleShared);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, qe_sample_kernel<T, STREAM>, a);
 }
 
 template <typename T>
@@ -773,40 +1017,19 @@ cudaError_t launch_sample_t(SampleArgs a, cudaStream_t s) {
   const int es = (int)sizeof(T);
   const int at_once = 2 * dev_info().sms;
   int cl = 1;
-  while (cl < 16 && (long long)a.V * es / cl > 80 * 1024) cl *= 2;
+  while (cl < 16 && (long long)a.V * es / cl > 72 * 1024) cl *= 2;
   while (cl < 16 && (long long)a.V * es / cl > 8 * 1024 && (long long)a.B * cl * 2 <= at_once) cl *= 2;
-  a.cluster = cl;
   const int n = 16 / es;
-  a.run = ((a.V + cl - 1) / cl + n - 1) / n * n;
-  a.smem_row = (a.run + 2 * n) * es;
-  a.smem_row = (a.smem_row + 127) / 128 * 128;
-  const int bytes = a.smem_row + (int)sizeof(SampleShared);
-  static std::atomic<bool> set[64];  // per device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!set[dev]) {
-    e = cudaFuncSetAttribute(qe_sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(qe_sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    set[dev] = true;
+  if (cl > 1 && (long long)a.B * cl > 2ll * at_once) {  // clusters in more than two waves
+    a.cluster = kStreamCluster;
+    a.run = ((a.V + a.cluster - 1) / a.cluster + n - 1) / n * n;
+    a.smem_row = 0;
+    return launch_sample_as<T, true>(a, s);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.B * cl));
-  cfg.blockDim = dim3(kSampleThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cl;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, qe_sample_kernel<T>, a);
+  a.cluster = cl;
+  a.run = ((a.V + cl - 1) / cl + n - 1) / n * n;
+  a.smem_row = ((a.run + 2 * n) * es + 127) / 128 * 128;
+  return launch_sample_as<T, false>(a, s);
 }
 
 }  // namespace

@@ -181,6 +181,39 @@ def test_a_row_does_not_depend_on_its_batch(q, cuda):
         assert t[0] == token[b] and l[0] == lp[b]
 
 
+@pytest.mark.parametrize("dtype,V,pad", [("f32", 90001, 3), ("bf16", 200003, 0), ("f16", 170000, 5)])
+def test_many_large_rows(q, cuda, dtype, V, pad):
+    # so many rows that they are read in passes instead of kept on chip: all settings side by
+    # side, masked, equal, infinite and NaN logits among them, rows that start off any boundary
+    import torch
+    B = 150
+    flat = torch.zeros(B * (V + pad) + 1, device="cuda", dtype=dt(dtype))
+    x = torch.as_strided(flat, (B, V), (V + pad, 1), 1 if pad else 0)
+    x.copy_(rows(B, V, dtype, 12))
+    ban = torch.rand((B, V), generator=torch.Generator(device="cuda").manual_seed(13), device="cuda") < 0.5
+    x[3::10] = torch.where(ban[3::10], -math.inf, x[3::10])
+    x[4::10] = torch.where(ban[4::10], math.nan, x[4::10])
+    x[5::30] = 1.5                      # all equal
+    x[15::30] = x[15::30].round()       # a few values
+    x[25::30, 77:V:1000] = math.inf
+    x[9] = -math.inf
+    rng = np.random.RandomState(3)
+    b = np.arange(B)
+    kw = dict(temperature=np.where(b % 7 == 3, 0.0, 0.3 + 1.5 * rng.rand(B)),
+              top_k=np.where(b % 3 == 0, np.exp(rng.uniform(0, np.log(V), B)).astype(int), 0),
+              top_p=np.where(b % 2 == 0, 0.3 + 0.7 * rng.rand(B), 1.0), min_p=np.where(b % 5 == 1, 0.1 * rng.rand(B), 0.0))
+    kw = {n: list(v) for n, v in kw.items()}
+    kw["top_k"] = [int(k) for k in kw["top_k"]]
+    for s in range(2):
+        u = np.random.RandomState(20 + s).rand(B).astype(np.float32)
+        token, lp = run(q, x, u, **kw)
+        check(x, u, token, lp, **kw)
+    # the same rows a few at a time (kept on chip) choose the same tokens
+    few = slice(60, 66)
+    t, l = run(q, x[few].clone(), u[few], **{n: v[few] for n, v in kw.items()})
+    assert np.array_equal(t, token[few]) and np.array_equal(l, lp[few])
+
+
 def test_outputs_beside_the_batch_stay(q, cuda):
     import torch
     x = rows(4, 777, "f32", 10)
