@@ -3,13 +3,14 @@
 //
 //   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = pos[axis(i)] f_i
 //
-// The operator reads T (n_q + 2 n_kv) head_dim elements and writes as many:
-// it is bound by HBM for prompts and by one launch's latency for a decode
-// step.  One CTA serves one token: the angles of its rotary_dim / 2 pairs are
-// computed once, into shared memory, and used by all its heads.  A thread's
-// item is 16 elements of a head (8 pairs, or 16 elements that are copied): two
-// 16-byte loads (four for fp32) and two 16-byte stores, requested before the
-// angles are waited for.
+// The operator reads T (n_q + 2 n_kv) head_dim elements and writes as many: it is
+// bound by HBM for prompts and by one launch's latency for a decode step.  The
+// angles of a token's rotary_dim / 2 pairs are computed once, into shared memory, and
+// used by all its heads.  A thread's item is 16 elements of a head in two runs of 8:
+// two 16-byte loads (four for fp32) and two 16-byte stores, requested an item ahead.
+// Measured: 1 token of 48 heads of 128 2.8 us, 256 tokens 3.7 us, 16384 tokens (403 MB)
+// 71 us, 5.7 TB/s (with a thread's 16 elements in one run, which leaves its neighbours'
+// requests half a sector each, 79 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -24,8 +25,9 @@
 namespace qe {
 namespace {
 
-constexpr int kKvThreads = 384;
+constexpr int kKvThreads = 256;
 constexpr int kMaxPairs = 128;  // head_dim 256 / 2
+constexpr int kKvTokens = 4;    // of one CTA at most
 
 struct KvArgs {
   const void* q;
@@ -41,7 +43,7 @@ struct KvArgs {
   const int32_t* seq;
   const int32_t* table;
   int* err;
-  int T, n_q, n_kv, D, rd, n_pages, n_seq, table_stride;
+  int T, n_q, n_kv, D, rd, n_pages, n_seq, table_stride, per_cta;
   FastDiv page;
   uint8_t axis[kMaxPairs];
 };
@@ -106,92 +108,147 @@ QE_DEV void store8(TC* p, const float (&x)[8]) {
                                             pack2<TC>(x[6], x[7]));
 }
 
+QE_DEV void turn_pair(float& a, float& b, float2 w) {
+  const float x = fmaf(a, w.x, -b * w.y);
+  b = fmaf(b, w.x, a * w.y);
+  a = x;
+}
+QE_DEV void adjacent8(float (&x)[8], const float2* w) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) turn_pair(x[2 * p], x[2 * p + 1], w[p]);
+}
+
+// One CTA: `a.per_cta` consecutive tokens.  The angles of all of them first (the items' loads
+// do not wait for them: each thread requests its first item before), then the items of
+// one token after the other.
 template <typename TI, typename TC, bool ADJ>
 __global__ void __launch_bounds__(kKvThreads) qe_kv_append_kernel(const __grid_constant__ KvArgs a) {
-  __shared__ float2 cs[kMaxPairs];
+  __shared__ float2 cs[kKvTokens * kMaxPairs];
+  __shared__ int place[kKvTokens][2];  // page and offset in it; page -1: none, -2: a padding row
   grid_dependency_wait();
   grid_launch_dependents();
-  const int t = blockIdx.x;
-  const int p = a.kv_pos[t];
-  if (p < 0) return;  // uniform over the CTA
+  const int t0 = blockIdx.x * a.per_cta, n = min(a.per_cta, a.T - t0);
   const int half = a.rd >> 1, per_head = a.D >> 4;
   const int items = (a.n_q + 2 * a.n_kv) * per_head;
 
-  // where the token goes
-  const int s = a.seq ? a.seq[t] : t;
-  const int col = (int)a.page.div((uint32_t)p);
-  int page = -1;
-  if (s >= 0 && s < a.n_seq && col < a.table_stride) page = a.table[(size_t)s * a.table_stride + col];
-  const bool ok = page >= 0 && page < a.n_pages;
-  const int off = p - col * (int)a.page.d;
-  if (!ok && threadIdx.x == 0) set_error(a.err, QE_ERR_INVALID_ARG);
-
-  for (int i = threadIdx.x; i < half; i += blockDim.x)
-    cs[i] = cos_sin(a.pos ? a.pos[(size_t)a.axis[i] * a.T + t] : p, a.inv_freq[i]);
-  __syncthreads();
-
-  for (int it = threadIdx.x; it < items; it += blockDim.x) {
-    const int head = it / per_head, e = (it - head * per_head) << 4;  // first of 16 elements, in item order
-    const TI* src;
-    TC* dst;
-    bool turn = true, write = true;
-    if (head < a.n_q) {
-      src = (const TI*)a.q + (size_t)t * a.q_stride + (size_t)head * a.D;
-      dst = (TC*)a.q_out + (size_t)t * a.q_out_stride + (size_t)head * a.D;
-    } else if (head < a.n_q + a.n_kv) {
-      const int h = head - a.n_q;
-      src = (const TI*)a.k + (size_t)t * a.k_stride + (size_t)h * a.D;
-      dst = (TC*)a.kc + (long long)page * a.k_page_stride + ((long long)h * a.page.d + off) * a.D;
-      write = ok;
-    } else {
-      const int h = head - a.n_q - a.n_kv;
-      src = (const TI*)a.v + (size_t)t * a.v_stride + (size_t)h * a.D;
-      dst = (TC*)a.vc + (long long)page * a.v_page_stride + ((long long)h * a.page.d + off) * a.D;
-      turn = false;
-      write = ok;
-    }
-    if (!write) continue;
-    turn = turn && e < a.rd;
-    // the two runs of 8: side by side, or a pair's two halves
-    const bool split = turn && !ADJ;
-    const int e0 = split ? e >> 1 : e, e1 = split ? e0 + half : e + 8;
+  struct Item {
     Raw8<TI> r0, r1;
-    r0.load(src + e0);
-    r1.load(src + e1);
+    int head, e0, e1;  // first elements of its two runs of 8
+    bool turn;         // a pair's two halves (half pairs); some of it is turned (adjacent pairs)
+  };
+  // Item `it` of token t.  Its two runs of 8 lie apart, so that the runs of neighbouring
+  // threads are neighbours: a pair's two halves, or halves of what is not split so.
+  auto load = [&](int t, int it, Item& x) {
+    x.head = it / per_head;
+    const int i = it - x.head * per_head;
+    const int rd = x.head < a.n_q + a.n_kv ? a.rd : 0;
+    if (ADJ) {
+      x.e0 = 8 * i;
+      x.e1 = x.e0 + (a.D >> 1);
+      x.turn = x.e0 < rd;
+    } else {
+      x.turn = 16 * i < rd;
+      x.e0 = x.turn ? 8 * i : rd + 8 * i - (rd >> 1);
+      x.e1 = x.e0 + ((x.turn ? rd : a.D - rd) >> 1);
+    }
+    const TI* src;
+    if (x.head < a.n_q) src = (const TI*)a.q + (size_t)t * a.q_stride + (size_t)x.head * a.D;
+    else if (x.head < a.n_q + a.n_kv) src = (const TI*)a.k + (size_t)t * a.k_stride + (size_t)(x.head - a.n_q) * a.D;
+    else src = (const TI*)a.v + (size_t)t * a.v_stride + (size_t)(x.head - a.n_q - a.n_kv) * a.D;
+    x.r0.load(src + x.e0);
+    x.r1.load(src + x.e1);
+  };
+  auto finish = [&](int t, int i, const Item& x) {
+    const int page = place[i][0], off = place[i][1];
+    if (page == -2) return;
+    TC* dst;
+    if (x.head < a.n_q) {
+      dst = (TC*)a.q_out + (size_t)t * a.q_out_stride + (size_t)x.head * a.D;
+    } else {
+      if (page < 0) return;
+      const bool is_k = x.head < a.n_q + a.n_kv;
+      const int h = x.head - a.n_q - (is_k ? 0 : a.n_kv);
+      dst = (TC*)(is_k ? a.kc : a.vc) + (long long)page * (is_k ? a.k_page_stride : a.v_page_stride) +
+            ((long long)h * a.page.d + off) * a.D;
+    }
     if constexpr (sizeof(TI) == 2 && std::is_same<TI, TC>::value) {
-      if (!turn) {  // the bits as they are (a NaN's too)
-        *reinterpret_cast<uint4*>(dst + e0) = r0.a;
-        *reinterpret_cast<uint4*>(dst + e1) = r1.a;
-        continue;
+      if (!x.turn) {  // the bits as they are (a NaN's too)
+        *reinterpret_cast<uint4*>(dst + x.e0) = x.r0.a;
+        *reinterpret_cast<uint4*>(dst + x.e1) = x.r1.a;
+        return;
       }
     }
-    float x[8], y[8];
-    r0.get(x);
-    r1.get(y);
-    if (turn) {
-      const int pair = e >> 1;
+    float u[8], v[8];
+    x.r0.get(u);
+    x.r1.get(v);
+    if (x.turn) {
+      const float2* w = cs + i * half;
+      if (ADJ) {
+        adjacent8(u, w + (x.e0 >> 1));
+        if (x.e1 < a.rd) adjacent8(v, w + (x.e1 >> 1));
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 w = cs[pair + j];
-        float& u = ADJ ? (j < 4 ? x[2 * (j & 3)] : y[2 * (j & 3)]) : x[j];
-        float& v = ADJ ? (j < 4 ? x[2 * (j & 3) + 1] : y[2 * (j & 3) + 1]) : y[j];
-        const float u2 = fmaf(u, w.x, -v * w.y), v2 = fmaf(v, w.x, u * w.y);
-        u = u2;
-        v = v2;
+        for (int p = 0; p < 8; ++p) turn_pair(u[p], v[p], w[x.e0 + p]);
       }
     }
-    store8(dst + e0, x);
-    store8(dst + e1, y);
+    store8(dst + x.e0, u);
+    store8(dst + x.e1, v);
+  };
+
+  // the first items are on their way while places and angles are worked out
+  Item x;
+  int i = 0, it = threadIdx.x;  // token of the CTA's, item of the token
+  auto settle = [&](int& ti, int& k) {
+    while (k >= items) {
+      k -= items;
+      ++ti;
+    }
+  };
+  settle(i, it);
+  if (i < n) load(t0 + i, it, x);
+  if ((int)threadIdx.x < n) {
+    const int t = t0 + threadIdx.x, p = a.kv_pos[t];
+    int page = -2, off = 0;
+    if (p >= 0) {
+      const int s = a.seq ? a.seq[t] : t, col = (int)a.page.div((uint32_t)p);
+      page = -1;
+      if (s >= 0 && s < a.n_seq && col < a.table_stride) page = a.table[(size_t)s * a.table_stride + col];
+      if (page < 0 || page >= a.n_pages) {
+        page = -1;
+        set_error(a.err, QE_ERR_INVALID_ARG);
+      }
+      off = p - col * (int)a.page.d;
+    }
+    place[threadIdx.x][0] = page;
+    place[threadIdx.x][1] = off;
+  }
+  for (int c = threadIdx.x; c < n * half; c += blockDim.x) {
+    const int j = c / half, pair = c - j * half;
+    cs[c] = cos_sin(a.pos ? a.pos[(size_t)a.axis[pair] * a.T + t0 + j] : a.kv_pos[t0 + j], a.inv_freq[pair]);
+  }
+  __syncthreads();
+  while (i < n) {
+    int next = i, next_it = it + blockDim.x;
+    settle(next, next_it);
+    Item y;
+    if (next < n) load(t0 + next, next_it, y);
+    finish(t0 + i, i, x);
+    x = y;
+    i = next;
+    it = next_it;
   }
 }
 
 template <typename TI, typename TC>
-cudaError_t launch_kv_t(const KvArgs& a, bool adjacent, cudaStream_t s) {
+cudaError_t launch_kv_t(KvArgs a, bool adjacent, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
+  // one token a CTA until the GPU is full, then several, whose items follow one another
+  // without a pause: 16384 tokens take 100 us by one, 88 by two, 79 by four and 82 by eight
   const int items = (a.n_q + 2 * a.n_kv) * (a.D >> 4);
+  a.per_cta = a.T >= 16 * dev_info().sms ? kKvTokens : 1;
   int threads = (items + 31) / 32 * 32;
   threads = threads < 64 ? 64 : threads > kKvThreads ? kKvThreads : threads;
-  cfg.gridDim = dim3((unsigned)a.T);
+  cfg.gridDim = dim3((unsigned)((a.T + a.per_cta - 1) / a.per_cta));
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
