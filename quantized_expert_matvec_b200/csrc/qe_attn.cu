@@ -180,6 +180,28 @@ QE_DEV void tmem_wait_ld(float (&v)[16]) {
 }
 QE_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+typedef unsigned long long u64;
+// two fp32 numbers in a register pair
+QE_DEV u64 pair(float lo, float hi) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+QE_DEV float2 unpair(u64 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+QE_DEV u64 fma_pair(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+QE_DEV u64 add_pair(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 QE_DEV float exp2_approx(float x) {  // 2^-22 relative; below 2^-126: 0
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -843,39 +865,43 @@ QE_DEV void soften_wide(const AttnArgs& a, const Segment& x, int seg, int n, int
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
   const uint32_t tmem = tmem_base + ((uint32_t)(32 * w) << 16), s_at = tmem + group * 128, o_at = tmem + 256 + group * 128;
   const int row = threadIdx.x;  // of the block: group * 128 + lane of the accumulator
-  float neg = kNoRef, l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+  float neg = kNoRef;
+  u64 sum[2] = {0, 0};  // l in four parts
 #pragma unroll 1
   for (int i = 0; i < x.n; ++i, ++n, ++tile) {
     wait_for(&sh.ws_full[group], n & 1, sh, a);  // the outputs of the tile before are complete then, too
     __syncwarp();
     tc_after();
     const uint4 live = *reinterpret_cast<const uint4*>(sh.live[tile & 7]);
-    const uint32_t words[4] = {live.x, live.y, live.z, live.w};
     const bool all = (live.x & live.y & live.z & live.w) == 0xffffffffu;
+    // half a row in registers at a time, read twice: the maximum, the exponentials and
+    // the sums of its columns have no order among them, and a whole row would spill
+    float v[4][16];
+    auto half_row = [&](int c) {
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_ld16(s_at + c * 64 + k * 16, v[k]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_wait_ld(v[k]);
+      if (!all) {
+        const uint32_t w0 = c ? live.z : live.x, w1 = c ? live.w : live.y;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (!(((k >> 1 ? w1 : w0) >> ((k & 1) * 16 + e)) & 1)) v[k][e] = -INFINITY;
+      }
+    };
     float top = -INFINITY;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      float v[16], u[16];
-      __syncwarp();
-      tmem_ld16(s_at + c * 32, v);
-      tmem_ld16(s_at + c * 32 + 16, u);
-      tmem_wait_ld(v);
-      tmem_wait_ld(u);
-      if (!all) {
-        const uint32_t m = c == 0 ? words[0] : c == 1 ? words[1] : c == 2 ? words[2] : words[3];
+    for (int c = 0; c < 2; ++c) {
+      half_row(c);
+      float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (!((m >> e) & 1)) v[e] = -INFINITY;
-          if (!((m >> (e + 16)) & 1)) u[e] = -INFINITY;
-        }
-      }
-      float t0 = fmaxf(v[0], u[0]), t1 = fmaxf(v[1], u[1]);
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int e = 2; e < 16; e += 2) {
-        t0 = fmaxf(t0, fmaxf(v[e], u[e]));
-        t1 = fmaxf(t1, fmaxf(v[e + 1], u[e + 1]));
-      }
-      top = fmaxf(top, fmaxf(t0, t1));
+        for (int e = 0; e < 16; e += 2) t[(e >> 1) & 3] = fmaxf(t[(e >> 1) & 3], fmaxf(v[k][e], v[k][e + 1]));
+      top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
     }
     top *= a.scale_log2;  // scale >= 0; 0 times an infinity gives NaN, which raises nothing
     const bool raise = top + neg > kSlack;
@@ -885,10 +911,9 @@ QE_DEV void soften_wide(const AttnArgs& a, const Segment& x, int seg, int n, int
         f = exp2_approx(-neg - top);
         neg = -top;
       }
-      l0 *= f;
-      l1 *= f;
-      l2 *= f;
-      l3 *= f;
+      const u64 f2 = pair(f, f);
+      sum[0] = fma_pair(sum[0], f2, 0);
+      sum[1] = fma_pair(sum[1], f2, 0);
       if (i > 0) {
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
@@ -902,38 +927,25 @@ QE_DEV void soften_wide(const AttnArgs& a, const Segment& x, int seg, int n, int
         }
       }
     }
+    // (a masked score is -inf and its numerator 0, unless nothing was ever seen: neg is
+    // 3e38 then, and -inf + 3e38 is -inf still)
+    const u64 scale2 = pair(a.scale_log2, a.scale_log2), neg2 = pair(neg, neg);
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      float v[16], u[16];
-      uint32_t pk[16];
-      __syncwarp();
-      tmem_ld16(s_at + c * 32, v);
-      tmem_ld16(s_at + c * 32 + 16, u);
-      tmem_wait_ld(v);
-      tmem_wait_ld(u);
+    for (int c = 0; c < 2; ++c) {
+      half_row(c);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        v[e] = exp2_approx(fmaf(v[e], a.scale_log2, neg));
-        u[e] = exp2_approx(fmaf(u[e], a.scale_log2, neg));
-      }
-      if (!all) {
-        const uint32_t m = c == 0 ? words[0] : c == 1 ? words[1] : c == 2 ? words[2] : words[3];
+      for (int k = 0; k < 2; ++k) {
+        uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (!((m >> e) & 1)) v[e] = 0.f;
-          if (!((m >> (e + 16)) & 1)) u[e] = 0.f;
+        for (int e = 0; e < 32; e += 2) {
+          float* x = &v[2 * k + (e >> 4)][e & 15];
+          const float2 y = unpair(fma_pair(pair(x[0], x[1]), scale2, neg2));
+          const float x0 = exp2_approx(y.x), x1 = exp2_approx(y.y);
+          sum[(e >> 1) & 1] = add_pair(sum[(e >> 1) & 1], pair(x0, x1));
+          pk[e >> 1] = pack2<T>(x0, x1);
         }
+        tmem_st16(s_at + c * 32 + k * 16, pk);  // over scores that have been read
       }
-#pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        l0 += v[e];
-        l1 += v[e + 1];
-        l2 += u[e];
-        l3 += u[e + 1];
-        pk[e / 2] = pack2<T>(v[e], v[e + 1]);
-        pk[8 + e / 2] = pack2<T>(u[e], u[e + 1]);
-      }
-      tmem_st16(s_at + c * 16, pk);  // over scores that have been read
     }
     tmem_wait_st();
     tc_before();
@@ -959,8 +971,9 @@ QE_DEV void soften_wide(const AttnArgs& a, const Segment& x, int seg, int n, int
   }
   if (row < x.rows) {
     float4* pml = reinterpret_cast<float4*>((x.b >= 0 ? a.ml_own : a.ml_prefix) + (row_at + row) * 4);
-    pml[0] = make_float4(-neg, l0, -neg, l1);
-    pml[1] = make_float4(-neg, l2, -neg, l3);
+    const float2 l0 = unpair(sum[0]), l1 = unpair(sum[1]);
+    pml[0] = make_float4(-neg, l0.x, -neg, l0.y);
+    pml[1] = make_float4(-neg, l1.x, -neg, l1.y);
   }
   tc_before();
 }
