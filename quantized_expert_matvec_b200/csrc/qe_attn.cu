@@ -110,6 +110,7 @@ struct AttnArgs {
   int rb_prefix, rb_own;  // row blocks per key head
   int own_rows;           // rows of an own block: min(G, kRows)
   float scale_log2;
+  int run;                // keys that lie behind one another: the largest power of two in page_size, at most 32
   FastDiv page, group;    // by the page size and by G
 };
 
@@ -211,6 +212,12 @@ QE_DEV float exp2_approx(float x) {  // 2^-22 relative; below 2^-126: 0
 // 16 bytes, or 16 zeros
 QE_DEV void cp_async16z(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+
+// 16 bytes at constant distances from both addresses
+template <int DST, int SRC>
+QE_DEV void cp_async16_at(uint32_t dst, unsigned long long src) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(DST), "n"(SRC) : "memory");
 }
 
 // ------------------------------------------------------------------ shares
@@ -440,6 +447,15 @@ struct Places {
   }
 };
 
+// f(integral_constant<int, 0>), f(<1>), ... f(<N - 1>)
+template <int N, typename F>
+QE_DEV void for_constants(F f) {
+  if constexpr (N > 0) {
+    for_constants<N - 1>(f);
+    f(std::integral_constant<int, N - 1>());
+  }
+}
+
 template <typename T, int D>
 QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned char* qs) {
   using Sh = Shape<D>;
@@ -447,11 +463,29 @@ QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned
   constexpr int RPI = 32 / CH;        // rows a warp instruction copies
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftWarps;
   const int sub = lane % CH, sub_row = lane / CH;
-  const uint32_t ring_u = smem_u32(ring) + (sub >> 3) * (kTile * 128) + (32 * w + sub_row) * 128;
+  // this lane's place in a stage: of row 32 w + RPI k + sub_row, k < PERIOD; later rows are
+  // whole swizzle periods of 1024 bytes further on
+  constexpr int PERIOD = 8 / RPI;
+  const uint32_t ring_u = smem_u32(ring) + (sub >> 3) * (kTile * 128) + 32 * w * 128;
+  uint32_t place[PERIOD];
+#pragma unroll
+  for (int k = 0; k < PERIOD; ++k)
+    place[k] = ring_u + (k * RPI + sub_row) * 128 + (((sub & 7) ^ ((k * RPI + sub_row) & 7)) << 4);
   const uint32_t q_u = smem_u32(qs);
   int stage = 0, phase = 1;  // fresh empty barriers count as free
   unsigned long long k_row = 0, v_row = 0, v_next = 0;  // this lane's rows of the tile
   uint32_t live = 0, v_live = 0;
+  // 32 rows that all exist, in runs of RUN that lie behind one another
+  auto copy_runs = [&](auto run, unsigned long long row, uint32_t at) {
+    constexpr int RUN = decltype(run)::value;
+    for_constants<32 / RUN>([&](auto g) {
+      const unsigned long long src = __shfl_sync(0xffffffffu, row, decltype(g)::value * RUN) + sub_row * (2 * D) + sub * 16;
+      for_constants<RUN / RPI>([&](auto i) {
+        constexpr int I = decltype(i)::value, it = decltype(g)::value * (RUN / RPI) + I;
+        cp_async16_at<it / PERIOD * 1024, I * RPI * 2 * D>(place[it % PERIOD] + at, src);
+      });
+    });
+  };
   auto load = [&](bool is_v) {
 #pragma unroll 1
     for (int p = 0; p < Sh::kParts; ++p) {
@@ -459,12 +493,18 @@ QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned
       const uint32_t lv = is_v ? v_live : live;
       wait_for(&sh.empty[stage], phase, sh, a);
       __syncwarp();
-      const uint32_t dst = ring_u + stage * Sh::kStage;
+      const uint32_t at = stage * Sh::kStage;
+      if (lv == 0xffffffffu && a.run >= 32) {
+        copy_runs(std::integral_constant<int, 32>(), row, at);
+      } else if (lv == 0xffffffffu && a.run >= 8) {
+        copy_runs(std::integral_constant<int, 8>(), row, at);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 32 / RPI; ++i) {
-        const int r = i * RPI + sub_row;
-        const unsigned long long at = __shfl_sync(0xffffffffu, row, r);
-        cp_async16z(dst + i * RPI * 128 + (((sub & 7) ^ (r & 7)) << 4), (const T*)at + sub * 8, (lv >> r) & 1);
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int r = i * RPI + sub_row;
+          const unsigned long long from = __shfl_sync(0xffffffffu, row, r);
+          cp_async16z(place[i % PERIOD] + at + i / PERIOD * 1024, (const T*)from + sub * 8, (lv >> r) & 1);
+        }
       }
       // every lane's copies arrive when they land; lane 0 arrives for what it wrote itself
       cp_async_mbar_arrive_noinc(&sh.full[stage]);
@@ -477,7 +517,8 @@ QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned
   };
   Reader reader;
   Segment x;
-  int left = 0, key0 = 0, n = 0, seg = -1, rows_before = 0;
+  int left = 0, key0 = 0, n = 0, seg = -1, rows_before = 0, page_next = -1;
+  auto page_at = [&](int key) { return key < x.kend ? __ldg(x.list + a.page.div((uint32_t)key)) : -1; };
   bool more = true;
   while (true) {
     bool first = false, v_first = false;
@@ -524,7 +565,8 @@ QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned
         }
       }
       const int key = key0 + 32 * w + lane;
-      const int page = key < x.kend ? __ldg(x.list + a.page.div((uint32_t)key)) : -1;
+      const int page = first ? page_at(key) : page_next;  // asked for a tile ahead
+      page_next = left > 1 ? page_at(key + kTile) : -1;
       const bool ok = page >= 0 && page < a.n_pages;
       if (key < x.kend && !ok) set_error(a.err, QE_ERR_INVALID_ARG);
       live = __ballot_sync(0xffffffffu, ok);
@@ -1392,6 +1434,8 @@ extern "C" QE_API int attn_decode_step(const qe_kv_cache* c, int B, int n_q, con
   a.scale_log2 = scale * kLog2e;
   a.page = fast_div((uint32_t)c->page_size);
   a.group = fast_div((uint32_t)a.G);
+  a.run = c->page_size & -c->page_size;
+  if (a.run > 32) a.run = 32;
   // a wide tile of two blocks of 128 rows takes about twice a narrow one's time
   a.prefix_cost = (long long)B * a.G > 128 && p.max_rows > 128 ? 2 : 1;
   const cudaError_t e = c->dtype == QE_BF16 ? launch_attn<__nv_bfloat16>(a, D, p.grid, (cudaStream_t)stream)
