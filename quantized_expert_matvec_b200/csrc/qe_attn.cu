@@ -26,9 +26,11 @@
 //   0-7   softmax, two groups of four: narrow segments alternate between them (the
 //         end of one overlaps the start of the next), a wide one's rows 0-127 and
 //         128-255 are one group's each;
-//   8-11  producers: K and V rows by cp.async from their pages into a ring of
-//         128-byte-swizzled tiles; keys that do not exist become zeros;
-//   12    one thread issues the products;
+//   8-11  producers, 32 keys of a tile each: K and V from their pages into a ring of
+//         128-byte-swizzled tiles, by TMA in boxes of 64 dims x 8 to 32 rows of a page, or
+//         row by row with cp.async where a page holds no such runs or some keys do not
+//         exist (they become zeros: a V row of NaN would not vanish against a P of 0);
+//   12    issues the products;
 //   13    one thread deals out the CTA's segments, through a ring of descriptors
 //         (each role working them out for itself made the code 160 KB and every
 //         role wait for its instructions).
@@ -36,6 +38,7 @@
 // when a score passes it by more than 2^8.  l is the sum of the fp32 numerators;
 // their rounding to the cache's dtype is the one that the second product's
 // operand type asks for.
+#include <cuda.h>  // types of the tensor map
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -110,7 +113,7 @@ struct AttnArgs {
   int rb_prefix, rb_own;  // row blocks per key head
   int own_rows;           // rows of an own block: min(G, kRows)
   float scale_log2;
-  int run;                // keys that lie behind one another: the largest power of two in page_size, at most 32
+  int run_bits;           // 2^run_bits keys lie behind one another: the power of two in page_size, at most 32; 0: no map
   FastDiv page, group;    // by the page size and by G
 };
 
@@ -130,28 +133,37 @@ QE_DEV uint32_t mma_idesc(int N, bool a_mn, bool b_mn) {
   return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
+// The products are issued by the whole warp together, of which one lane is elected for each:
+// their operands live in uniform registers, and a lane alone in a branch has to move each
+// of them there first (128 clocks a product, measured, whatever its size).
 QE_DEV void mma_issue(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, e;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " elect.sync _|e, 0xffffffff;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
+}
+// the same with A in tensor memory
+QE_DEV void mma_issue_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
+      " elect.sync _|e, 0xffffffff;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
       "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
       : "memory");
 }
 QE_DEV void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+      : "memory");
 }
+// A value that is the same in all lanes, told so to the compiler.
+template <typename V>
+QE_DEV V uniform(V v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 QE_DEV void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 QE_DEV void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 QE_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// the same with A in tensor memory
-QE_DEV void mma_issue_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
-      : "memory");
-}
 
 // 16 columns of the warp's 32 lanes
 QE_DEV void tmem_ld16(uint32_t a, float (&v)[16]) {
@@ -214,12 +226,13 @@ QE_DEV void cp_async16z(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
 
-// 16 bytes at constant distances from both addresses
-template <int DST, int SRC>
-QE_DEV void cp_async16_at(uint32_t dst, unsigned long long src) {
-  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(DST), "n"(SRC) : "memory");
+// A box of the cache's tensor map {dims, rows of a page, pages}; x is a multiple of 64 dims.
+QE_DEV void tma_box(uint32_t dst, const CUtensorMap* map, int x, int row, int page, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(row), "r"(page), "r"(smem_u32(bar))
+      : "memory");
 }
-
 // ------------------------------------------------------------------ shares
 
 // x * num / den, with 32-bit arithmetic where the product has 32 bits (a 64-bit
@@ -447,17 +460,9 @@ struct Places {
   }
 };
 
-// f(integral_constant<int, 0>), f(<1>), ... f(<N - 1>)
-template <int N, typename F>
-QE_DEV void for_constants(F f) {
-  if constexpr (N > 0) {
-    for_constants<N - 1>(f);
-    f(std::integral_constant<int, N - 1>());
-  }
-}
-
 template <typename T, int D>
-QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned char* qs) {
+QE_DEV void produce(const AttnArgs& a, const CUtensorMap* k_map, const CUtensorMap* v_map, Shared& sh, unsigned char* ring,
+                    unsigned char* qs) {
   using Sh = Shape<D>;
   constexpr int CH = Sh::kDims / 8;   // 16-byte pieces of a row of a stage
   constexpr int RPI = 32 / CH;        // rows a warp instruction copies
@@ -473,19 +478,11 @@ QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned
     place[k] = ring_u + (k * RPI + sub_row) * 128 + (((sub & 7) ^ ((k * RPI + sub_row) & 7)) << 4);
   const uint32_t q_u = smem_u32(qs);
   int stage = 0, phase = 1;  // fresh empty barriers count as free
-  unsigned long long k_row = 0, v_row = 0, v_next = 0;  // this lane's rows of the tile
+  // this lane's row of the tile, of K and of the V that follows later: address, and place in the map
+  unsigned long long k_row = 0, v_row = 0, v_next = 0;
+  int k_page = 0, k_in_page = 0, v_page = 0, v_in_page = 0, issued = 0;
   uint32_t live = 0, v_live = 0;
-  // 32 rows that all exist, in runs of RUN that lie behind one another
-  auto copy_runs = [&](auto run, unsigned long long row, uint32_t at) {
-    constexpr int RUN = decltype(run)::value;
-    for_constants<32 / RUN>([&](auto g) {
-      const unsigned long long src = __shfl_sync(0xffffffffu, row, decltype(g)::value * RUN) + sub_row * (2 * D) + sub * 16;
-      for_constants<RUN / RPI>([&](auto i) {
-        constexpr int I = decltype(i)::value, it = decltype(g)::value * (RUN / RPI) + I;
-        cp_async16_at<it / PERIOD * 1024, I * RPI * 2 * D>(place[it % PERIOD] + at, src);
-      });
-    });
-  };
+  const uint32_t ring_at = smem_u32(ring);
   auto load = [&](bool is_v) {
 #pragma unroll 1
     for (int p = 0; p < Sh::kParts; ++p) {
@@ -494,10 +491,17 @@ QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned
       wait_for(&sh.empty[stage], phase, sh, a);
       __syncwarp();
       const uint32_t at = stage * Sh::kStage;
-      if (lv == 0xffffffffu && a.run >= 32) {
-        copy_runs(std::integral_constant<int, 32>(), row, at);
-      } else if (lv == 0xffffffffu && a.run >= 8) {
-        copy_runs(std::integral_constant<int, 8>(), row, at);
+      if (lv == 0xffffffffu && a.run_bits >= 3) {
+        // lane l: run l mod (32 / run) of the warp's rows, 64 dims l / (32 / run)
+        const int runs = 32 >> a.run_bits, from = (lane & (runs - 1)) << a.run_bits, block = lane >> (5 - a.run_bits);
+        const int page = __shfl_sync(0xffffffffu, is_v ? v_page : k_page, from);
+        const int in_page = __shfl_sync(0xffffffffu, is_v ? v_in_page : k_in_page, from);
+        if (lane == 0) mbar_arrive_expect_tx(&sh.full[stage], 32 * Sh::kDims * 2);
+        __syncwarp();
+        if (block < Sh::kDims / 64)
+          tma_box(ring_at + at + block * (kTile * 128) + (32 * w + from) * 128, is_v ? v_map : k_map,
+                  p * Sh::kDims + block * 64, in_page, page, &sh.full[stage]);
+        mbar_arrive(&sh.full[stage]);  // every lane: the barrier counts 33 a warp
       } else {
 #pragma unroll
         for (int i = 0; i < 32 / RPI; ++i) {
@@ -505,10 +509,11 @@ QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned
           const unsigned long long from = __shfl_sync(0xffffffffu, row, r);
           cp_async16z(place[i % PERIOD] + at + i / PERIOD * 1024, (const T*)from + sub * 8, (lv >> r) & 1);
         }
+        // every lane's copies arrive when they land; lane 0 arrives for what it wrote itself
+        cp_async_mbar_arrive_noinc(&sh.full[stage]);
+        if (lane == 0) mbar_arrive(&sh.full[stage]);
       }
-      // every lane's copies arrive when they land; lane 0 arrives for what it wrote itself
-      cp_async_mbar_arrive_noinc(&sh.full[stage]);
-      if (lane == 0) mbar_arrive(&sh.full[stage]);
+      ++issued;
       if (++stage == Sh::kStages) {
         stage = 0;
         phase ^= 1;
@@ -550,18 +555,17 @@ QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned
         rows_before = x.rows;
         const int fill = wide ? (x.rows + 127) & ~127 : (x.rows + 15) & ~15;
         const uint32_t dst = q_u + (!whole && (seg & 1) ? Sh::kQLines / 2 * 128 : 0);
-#pragma unroll 1
-        for (int e = threadIdx.x - 32 * kSoftWarps; e < fill * (D / 8); e += 32 * kProdWarps) {
-          const int r = e / (D / 8), ch = e % (D / 8);
-          const T* src = (const T*)a.q;
-          if (r < x.rows) {
-            const int f = x.row0 + r, fb = a.group.div(f);
-            src += x.b >= 0 ? (size_t)x.b * a.q_stride + (size_t)(x.h * a.G + f) * D
-                            : (size_t)fb * a.q_stride + (size_t)(x.h * a.G + f - fb * a.G) * D;
-          }
-          const uint32_t line = wide ? (r >> 7) * (D * 256) + (ch >> 3) * (128 * 128) + (r & 127) * 128
-                                     : (ch >> 3) * (Sh::kQLines * 128) + r * 128;
-          cp_async16z(dst + line + (((ch & 7) ^ (r & 7)) << 4), src + ch * 8, r < x.rows);
+        // a thread keeps its 16-byte piece and steps through the rows, 128 / (D / 8) at a time
+        constexpr int STEP = 32 * kProdWarps / (D / 8);
+        const int tid = threadIdx.x - 32 * kSoftWarps, ch = tid % (D / 8), r0 = tid / (D / 8);
+        const T* q_head = (const T*)a.q + (size_t)x.h * a.G * D + ch * 8 + (x.b >= 0 ? (size_t)x.b * a.q_stride : 0);
+        const uint32_t col = dst + (ch >> 3) * ((wide ? 128 : Sh::kQLines) * 128);
+#pragma unroll 4
+        for (int r = r0; r < fill; r += STEP) {
+          const int f = x.row0 + r, fb = x.b >= 0 ? 0 : (int)a.group.div((uint32_t)f);
+          const T* src = q_head + (long long)fb * a.q_stride + (f - fb * a.G) * D;
+          const uint32_t line = wide ? (r >> 7) * (D * 256) + (r & 127) * 128 : r * 128;
+          cp_async16z(col + line + (((ch & 7) ^ (r & 7)) << 4), r < x.rows ? src : (const T*)a.q, r < x.rows);
         }
       }
       const int key = key0 + 32 * w + lane;
@@ -570,7 +574,9 @@ QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned
       const bool ok = page >= 0 && page < a.n_pages;
       if (key < x.kend && !ok) set_error(a.err, QE_ERR_INVALID_ARG);
       live = __ballot_sync(0xffffffffu, ok);
-      const long long in_page = ((long long)x.h * a.page.d + (key - (int)a.page.div((uint32_t)key) * (int)a.page.d)) * D;
+      k_page = page;
+      k_in_page = x.h * (int)a.page.d + key - (int)a.page.div((uint32_t)key) * (int)a.page.d;
+      const long long in_page = (long long)k_in_page * D;
       k_row = (unsigned long long)((const T*)a.kc + (ok ? page * a.k_page_stride + in_page : 0));
       v_next = (unsigned long long)((const T*)a.vc + (ok ? page * a.v_page_stride + in_page : 0));
       if (lane == 0) sh.live[n & 7][w] = live;
@@ -578,14 +584,23 @@ QE_DEV void produce(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned
     }
     if (!more) break;
     v_row = v_next;
+    v_page = k_page;
+    v_in_page = k_in_page;
     v_live = live;
     key0 += kTile;
     --left;
     ++n;
   }
   cp_async_wait_all();
+  // nothing may be in flight when the CTA leaves (after a wait that gave up, the last stages could be)
+  for (int i = max(0, issued - Sh::kStages); i < issued; ++i) {
+    const uint64_t deadline = gtimer() + a.budget_ns;
+    while (!mbar_try_wait(&sh.full[i % Sh::kStages], (i / Sh::kStages) & 1))
+      if (gtimer() > deadline) break;
+  }
 }
 
+// One warp, every value in it uniform.
 template <typename T, int D>
 QE_DEV void multiply(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigned char* qs, unsigned char* ps,
                      uint32_t tmem) {
@@ -594,6 +609,7 @@ QE_DEV void multiply(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigne
   // stage number `place * kParts + part` of the producers' order
   auto take = [&](int at) {
     wait_for(&sh.full[at % Sh::kStages], (at / Sh::kStages) & 1, sh, a);
+    __syncwarp();
     fence_async_smem();  // the copies wrote through the generic proxy, the products read through the async one
     tc_after();
     return ring_u + at % Sh::kStages * Sh::kStage;
@@ -619,6 +635,7 @@ QE_DEV void multiply(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigne
   };
   auto narrow_outputs = [&](int m, int rows, int seg, bool first, int v_place) {
     wait_turn(sh.p_full, m, sh, a);
+    __syncwarp();
     const uint32_t idesc = mma_idesc<T>((rows + 15) & ~15, true, true), d = tmem + 256 + (seg & 1) * 128;
     const uint32_t p_at = desc_low(p_u + (m & 1) * Sh::kP, kTile * 128);
 #pragma unroll 1
@@ -659,7 +676,12 @@ QE_DEV void multiply(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigne
 
   Reader reader;
   Segment x;
-  reader.next(x, sh, a, false, true);
+  auto next_segment = [&](Segment& y) {
+    reader.next(y, sh, a, true, (threadIdx.x & 31) == 0);
+    y.n = uniform(y.n);
+    y.rows = uniform(y.rows);
+  };
+  next_segment(x);
   bool wide_before = false;
   int wide_n = 0;  // wide tiles so far, by which the phases of wp_full go (block 1 may have had fewer)
   int wide_n1 = 0;
@@ -689,7 +711,7 @@ QE_DEV void multiply(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigne
         }
         bool v_first = false;
         if (i == x.n - 1) {
-          reader.next(y, sh, a, false, true);
+          next_segment(y);
           v_first = y.n == 0 || y.rows > kNarrow;
         }
         pl.step(v_first);
@@ -708,12 +730,13 @@ QE_DEV void multiply(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigne
       for (int i = 0; i < x.n; ++i) {
         bool v_first = false;
         if (i == x.n - 1) {
-          reader.next(y, sh, a, false, true);
+          next_segment(y);
           v_first = y.n == 0 || y.rows <= kNarrow;
         }
         pl.step(v_first);
         for (int blk = 0; blk < blocks; ++blk) {
           wait_for(&sh.wp_full[blk], (blk ? wide_n1 : wide_n) & 1, sh, a);
+          __syncwarp();
           tc_after();
           wide_outputs(blk, blk == blocks - 1, i == 0, pl.v);
           if (i + 1 < x.n) wide_scores(blk, blk == blocks - 1);
@@ -728,6 +751,7 @@ QE_DEV void multiply(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigne
     x = y;
   }
   // whatever happened, nothing is in flight when this returns
+  __syncwarp();
   mma_commit(&sh.drained);
   const uint64_t deadline = gtimer() + a.budget_ns;
   while (!mbar_try_wait_sleep(&sh.drained, 0, 10000u))
@@ -1050,7 +1074,8 @@ QE_DEV void soften(const AttnArgs& a, Shared& sh, unsigned char* ps, uint32_t tm
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kAttnThreads, 1) qe_attn_part_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, 1) qe_attn_part_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap k_map,
+                        const __grid_constant__ CUtensorMap v_map) {
   using Sh = Shape<D>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(16) Shared sh;
@@ -1157,9 +1182,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) qe_attn_part_kernel(const __g
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
       if (warp < kSoftWarps + kProdWarps) {
-        produce<T, D>(a, sh, ring, qs);
+        produce<T, D>(a, &k_map, &v_map, sh, ring, qs);
       } else if (warp == 12) {
-        if (lane == 0) multiply<T, D>(a, sh, ring, qs, ps, tmem);
+        multiply<T, D>(a, sh, ring, qs, ps, uniform(tmem));
         __syncwarp();
       } else if (warp == 13) {
         if (lane == 0) deal_out<D>(a, deal, t0, t1, sh.found, sh.found_len, sh.found_start, cap, sh);
@@ -1188,34 +1213,22 @@ __global__ void __launch_bounds__(128) qe_attn_join_kernel(const __grid_constant
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp % WPR;
   const int rows = a.B * a.n_q, row = blockIdx.x * (4 / WPR) + warp / WPR;
   const bool real = row < rows;
-  const int b = real ? row / a.n_q : 0, hq = row - b * a.n_q, h = hq / a.G, g = hq - h * a.G;
-  const int kv = real ? a.kv_len[b] : -1;
-  int g0 = 0, np = 0, c0 = 0, no = 0;  // first group and CTA that hold segments, and how many
-  if (kv >= 0 && a.prefix_tiles > 0) {
-    const int2 r = a.prefix_groups[h];
-    g0 = r.x;
-    np = r.y - r.x + 1;
-  }
+  const int at_row = real ? row : 0, b = at_row / a.n_q, hq = at_row - b * a.n_q, h = hq / a.G, g = hq - h * a.G;
+  // what says where the row's segments are, in one round of loads
   const int unit = (b * a.n_kv + h) * a.rb_own + g / max_rows;
-  if (kv > 0 && a.table_stride > 0) {
-    const int2 r = a.own_ctas[unit];
-    c0 = r.x;
-    no = r.y - r.x + 1;
-  }
-  // segment i of this row: offset of its row, or of the first row of all if the CTA had no own tiles
-  auto where = [&](int i, const float2** ml, const float** o) {
-    size_t at;
-    if (i < np) {
-      at = (size_t)(g0 + i + h) * a.B * a.G + (size_t)b * a.G + g;
-      *ml = a.ml_prefix + at * 4;
-      *o = a.part_prefix + at * D;
-      return true;
-    }
-    const int c = c0 + i - np;
-    at = (size_t)(c + unit) * a.own_rows + g % max_rows;
-    *ml = a.ml_own + at * 4;
-    *o = a.part_own + at * D;
-    return a.own_start[c] < a.own_start[c + 1];
+  const int kv = real ? a.kv_len[b] : -1;
+  const int2 groups = a.prefix_tiles > 0 ? a.prefix_groups[h] : make_int2(0, -1);
+  const int2 ctas = a.table_stride > 0 ? a.own_ctas[unit] : make_int2(0, -1);
+  const int g0 = groups.x, np = kv >= 0 ? groups.y - groups.x + 1 : 0;
+  const int c0 = ctas.x, no = kv > 0 ? ctas.y - ctas.x + 1 : 0;  // (a row of no keys: an old or no value, not used)
+  // segment i of this row; false if that CTA had no own tiles (its slot holds anything then)
+  auto where = [&](int i, const float2** ml, const float** o, bool* has) {
+    const bool prefix = i < np;
+    const int c = prefix ? 0 : c0 + i - np;
+    const size_t at = prefix ? (size_t)(g0 + i + h) * a.B * a.G + (size_t)b * a.G + g : (size_t)(c + unit) * a.own_rows + g % max_rows;
+    *ml = (prefix ? a.ml_prefix : a.ml_own) + at * 4;
+    *o = (prefix ? a.part_prefix : a.part_own) + at * D;
+    *has = a.own_start[c] < a.own_start[c + 1] || prefix;
   };
   constexpr int E = D / 32;
   float acc[E];
@@ -1231,11 +1244,9 @@ __global__ void __launch_bounds__(128) qe_attn_join_kernel(const __grid_constant
     bool has = false;
     if (i < np + no) {
       const float2* p;
-      has = where(i, &p, &o);
-      if (has) {
-        const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 2);
-        ml = make_float2(u.x, (u.y + u.w) + (v.y + v.w));
-      }
+      where(i, &p, &o, &has);
+      const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 2);
+      if (has) ml = make_float2(u.x, (u.y + u.w) + (v.y + v.w));
     }
     const float top = fmaxf(m, warp_max(ml.x)), f0 = exp2_approx(m - top), f = has ? exp2_approx(ml.x - top) : 0.f;
     m = top;
@@ -1323,8 +1334,37 @@ AttnPlan attn_plan(int n_kv, int n_q, int D, int B, int sms) {
   return p;
 }
 
+// Tensor map of one half of the cache, {head_dim, n_kv * page_size, n_pages}, in boxes
+// of 64 dims x `rows`.  False if there is none (the kernel then copies by rows).
+bool cache_map(CUtensorMap* map, const qe_kv_cache* c, void* base, int64_t page_stride, int rows) {
+  typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<void*> entry{nullptr};
+  void* fn = entry;
+  if (!fn) {
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess || !fn) {
+      (void)cudaGetLastError();
+      return false;
+    }
+    entry = fn;
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->n_kv * c->page_size, (cuuint64_t)c->n_pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)c->head_dim * 2, (cuuint64_t)page_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1}, step[3] = {1, 1, 1};
+  return ((Encode)fn)(map, c->dtype == QE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base,
+                      dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct CacheMaps {
+  CUtensorMap k, v;
+};
+
 template <typename T, int D>
-cudaError_t launch_attn_t(const AttnArgs& a, int grid, cudaStream_t s) {
+cudaError_t launch_attn_t(const AttnArgs& a, const CacheMaps& m, int grid, cudaStream_t s) {
   static std::atomic<bool> set[64];  // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1345,7 +1385,7 @@ cudaError_t launch_attn_t(const AttnArgs& a, int grid, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, qe_attn_part_kernel<T, D>, a);
+  e = cudaLaunchKernelEx(&cfg, qe_attn_part_kernel<T, D>, a, m.k, m.v);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)a.B * a.n_q;
   cfg.blockDim = dim3(128);
@@ -1360,10 +1400,10 @@ cudaError_t launch_attn_t(const AttnArgs& a, int grid, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t launch_attn(const AttnArgs& a, int D, int grid, cudaStream_t s) {
-  if (D == 64) return launch_attn_t<T, 64>(a, grid, s);
-  if (D == 128) return launch_attn_t<T, 128>(a, grid, s);
-  return launch_attn_t<T, 256>(a, grid, s);
+cudaError_t launch_attn(const AttnArgs& a, const CacheMaps& m, int D, int grid, cudaStream_t s) {
+  if (D == 64) return launch_attn_t<T, 64>(a, m, grid, s);
+  if (D == 128) return launch_attn_t<T, 128>(a, m, grid, s);
+  return launch_attn_t<T, 256>(a, m, grid, s);
 }
 
 int check_attn_shape(const qe_kv_cache* c, int n_q, int B) {
@@ -1434,12 +1474,16 @@ extern "C" QE_API int attn_decode_step(const qe_kv_cache* c, int B, int n_q, con
   a.scale_log2 = scale * kLog2e;
   a.page = fast_div((uint32_t)c->page_size);
   a.group = fast_div((uint32_t)a.G);
-  a.run = c->page_size & -c->page_size;
-  if (a.run > 32) a.run = 32;
   // a wide tile of two blocks of 128 rows takes about twice a narrow one's time
   a.prefix_cost = (long long)B * a.G > 128 && p.max_rows > 128 ? 2 : 1;
-  const cudaError_t e = c->dtype == QE_BF16 ? launch_attn<__nv_bfloat16>(a, D, p.grid, (cudaStream_t)stream)
-                                            : launch_attn<__half>(a, D, p.grid, (cudaStream_t)stream);
+  CacheMaps m{};
+  int bits = 0;
+  while (bits < 5 && !((c->page_size >> bits) & 1)) ++bits;
+  if (bits >= 3 && c->n_pages > 0 && cache_map(&m.k, c, c->k, c->k_page_stride, 1 << bits) &&
+      cache_map(&m.v, c, c->v, c->v_page_stride, 1 << bits))
+    a.run_bits = bits;
+  const cudaError_t e = c->dtype == QE_BF16 ? launch_attn<__nv_bfloat16>(a, m, D, p.grid, (cudaStream_t)stream)
+                                            : launch_attn<__half>(a, m, D, p.grid, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "attn_decode_step launch");
   return QE_OK;
 }
