@@ -32,9 +32,9 @@ def append(q, c=None, rope=None, T=2, n_q=4, qp=16 * M, kp=17 * M, vp=18 * M, dt
 
 
 def attend(q, c=None, B=2, n_q=4, qp=16 * M, qs=512, prefix=None, prefix_len=0, table=21 * M, stride=4, kv_len=20 * M,
-           out=19 * M, os=512, lse=None, ws=22 * M, ws_bytes=1 << 40):
+           out=19 * M, os=512, lse=None, ws=22 * M, ws_bytes=1 << 40, scale=0.1):
     c = c if c is not None else cache(q)
-    return q.lib.attn_decode_step(ctypes.byref(c), B, n_q, qp, qs, prefix, prefix_len, table, stride, kv_len, 0.1, out,
+    return q.lib.attn_decode_step(ctypes.byref(c), B, n_q, qp, qs, prefix, prefix_len, table, stride, kv_len, scale, out,
                                   os, lse, ws, ws_bytes, None)
 
 
@@ -91,7 +91,7 @@ def test_append_refuses_rotations(q, kw, what):
     (dict(kv_len=None), "kv_len"), (dict(qp=16 * M + 2), "q is not"), (dict(out=None), "out is NULL"),
     (dict(qs=520 + 4), "strides"), (dict(os=504), "strides"), (dict(out=16 * M + 512), "overlaps"),
     (dict(ws=None), "workspace"), (dict(ws=22 * M + 128), "workspace"), (dict(ws_bytes=1024), "too small"),
-    (dict(lse=2), "lse"),
+    (dict(lse=2), "lse"), (dict(scale=-0.1), "scale"), (dict(scale=float("nan")), "scale"), (dict(scale=float("inf")), "scale"),
 ])
 def test_attention_refuses(q, kw, what):
     assert attend(q, **kw) == q.QE_ERR_INVALID_ARG
