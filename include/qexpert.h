@@ -473,7 +473,8 @@ typedef struct {
  * Arithmetic fp32; each element is rounded once, to the cache's dtype.  A
  * token whose seq, column or page is out of range is not appended (its q is
  * still rotated) and QE_ERR_INVALID_ARG is recorded in the workspace.  Two
- * tokens of one call must not name the same place.  dev_ws: any workspace
+ * tokens of one call must not name the same place; inputs and q_out must not
+ * overlap the cache's pages.  dev_ws: any workspace
  * with a control block (256 bytes or more).  One launch. */
 QE_API int attn_kv_append(const qe_kv_cache* cache, const qe_rope* rope, int T, int n_q, const void* q, const void* k,
                           const void* v, int in_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride, void* q_out,
@@ -501,7 +502,7 @@ QE_API size_t attn_workspace_bytes(const qe_kv_cache* cache, int n_q, int B);
  *     Negative: a padding row, whose out and lse are left as they were.
  *   lse fp32 [B][n_q] device or NULL: ln sum_j exp(scale q . k_j).
  * Several query tokens of one sequence are several rows with the same pages
- * and kv_len one apart.  scale is finite and >= 0.  n_q % n_kv == 0, n_q <= 1024, B <= 4096,
+ * and kv_len one apart.  scale is in [0, 2^64].  n_q % n_kv == 0, n_q <= 1024, B <= 4096,
  * table_stride * page_size and prefix_len < 2^30.  Scores, softmax statistics
  * and sums are fp32; the softmax numerators are rounded to the cache's dtype
  * for the product with v.  A kv_len beyond the table is cut to it, a key on a

@@ -1442,7 +1442,8 @@ extern "C" QE_API int attn_decode_step(const qe_kv_cache* c, int B, int n_q, con
   if (prefix_len < 0 || prefix_len >= 1 << 30) return fail(QE_ERR_INVALID_ARG, "prefix_len must be in [0, 2^30) (got %d)", prefix_len);
   if (table_stride < 0 || (int64_t)table_stride * c->page_size >= 1ll << 30)
     return fail(QE_ERR_INVALID_ARG, "table_stride * page_size must be in [0, 2^30)");
-  if (!(scale >= 0.f && scale <= 3.0e38f)) return fail(QE_ERR_INVALID_ARG, "scale must be finite and >= 0 (got %g)", scale);
+  // at 0x1p64 a scale times log2 e is far from the end of fp32
+  if (!(scale >= 0.f && scale <= 0x1p64f)) return fail(QE_ERR_INVALID_ARG, "scale must be in [0, 2^64] (got %g)", scale);
   if (B == 0) return QE_OK;
   const int D = c->head_dim;
   if ((rc = check_ptr(q, "q", false, 16)) || (rc = check_ptr(out, "out", false, 16)) || (rc = check_ptr(kv_len, "kv_len")) ||

@@ -92,6 +92,7 @@ def test_append_refuses_rotations(q, kw, what):
     (dict(qs=520 + 4), "strides"), (dict(os=504), "strides"), (dict(out=16 * M + 512), "overlaps"),
     (dict(ws=None), "workspace"), (dict(ws=22 * M + 128), "workspace"), (dict(ws_bytes=1024), "too small"),
     (dict(lse=2), "lse"), (dict(scale=-0.1), "scale"), (dict(scale=float("nan")), "scale"), (dict(scale=float("inf")), "scale"),
+    (dict(scale=2.5e38), "scale"),  # its product with log2 e is infinite
 ])
 def test_attention_refuses(q, kw, what):
     assert attend(q, **kw) == q.QE_ERR_INVALID_ARG

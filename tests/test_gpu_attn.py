@@ -435,6 +435,24 @@ def test_another_stream(q, cuda):
     assert torch.equal(out, want) and torch.equal(lse, lse2)
 
 
+def test_two_calls_at_once(q, cuda):
+    """Two streams, each call with a workspace of its own: neither sees the other."""
+    import torch
+    a = attend_inputs("bf16", 128, 2, 4, 16, 300, [50, 3, 900], seed=12)
+    b = attend_inputs("bf16", 64, 2, 8, 32, 0, [1, 700, 0, 129, 2000], seed=14)
+    want = [run_attend(q, d)[:2] for d in (a, b)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(8):
+        for i, d in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run_attend(q, d))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse, ws in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
 def test_empty_batch(q, cuda):
     import torch
     d = attend_inputs("bf16", 64, 1, 2, 16, 0, [3], seed=13)
