@@ -508,7 +508,9 @@ QE_DEV void produce(const AttnArgs& a, const CUtensorMap* k_map, const CUtensorM
         if (block < Sh::kDims / 64)
           tma_box(ring_at + at + block * (kTile * 128) + (32 * w + from) * 128, is_v ? v_map : k_map,
                   p * Sh::kDims + block * 64, in_page, page, &sh.full[stage]);
-        mbar_arrive(&sh.full[stage]);  // every lane: the barrier counts 33 a warp
+        // Every lane (the barrier counts 33 a warp), once its cp.async have landed: on a segment's
+        // first tile its queries are among them, and no other barrier says that they are there.
+        cp_async_mbar_arrive_noinc(&sh.full[stage]);
       } else {
 #pragma unroll
         for (int i = 0; i < 32 / RPI; ++i) {

@@ -453,6 +453,34 @@ def test_two_calls_at_once(q, cuda):
             assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
 
 
+@pytest.mark.parametrize("D,G,prefix,lens", [
+    (128, 64, 0, [130] * 600), (64, 16, 0, [200] * 900), (256, 32, 0, [70, 129] * 300), (128, 2, 4000, [0] * 900),
+], ids=["64_rows", "16_rows", "d256", "prefix"])
+def test_queries_that_arrive_after_the_keys(q, cuda, D, G, prefix, lens):
+    """Many segments a multiprocessor whose keys lie in L2 (every row has the same pages) and whose
+    queries come from memory: a product must not begin before its queries have landed."""
+    import torch
+    d = attend_inputs("bf16", D, 1, G, 16, prefix, lens[:2], seed=15)
+    g = torch.Generator(device="cuda").manual_seed(16)
+    d["B"], d["lens"] = len(lens), lens
+    d["tb"] = np.repeat(d["tb"][-1:], len(lens), axis=0)
+    kc = q.KVCache(d["kp"], d["vp"])
+    ws = q.attn_workspace(kc, G, d["B"])
+    cold = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")  # twice the L2 cache
+    first = torch.randn((d["B"], G, D), generator=g, device="cuda").to(torch.bfloat16)
+    want = {}
+    for trial in range(12):
+        d["q"] = first if trial % 2 == 0 else -first  # what an earlier segment left is never right
+        cold.fill_(trial)
+        out, lse, _ = run_attend(q, d, ws=ws)
+        if trial < 2:
+            want[trial] = out, lse
+            check_attend(d, out, lse, rows=range(trial, d["B"], 37))
+        else:
+            assert torch.equal(out, want[trial % 2][0]) and torch.equal(lse, want[trial % 2][1])
+    assert q.qe_workspace_status(ws) == q.QE_OK
+
+
 def test_empty_batch(q, cuda):
     import torch
     d = attend_inputs("bf16", 64, 1, 2, 16, 0, [3], seed=13)
