@@ -978,7 +978,7 @@ QE_DEV void soften_wide(const AttnArgs& a, const Segment& x, int seg, int n, int
         for (int e = 0; e < 16; e += 2) t[(e >> 1) & 3] = fmaxf(t[(e >> 1) & 3], fmaxf(v[k][e], v[k][e + 1]));
       top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
     }
-    top *= a.scale_log2;  // scale >= 0; 0 times an infinity gives NaN, which raises nothing
+    top *= a.scale_log2;  // scale > 0
     const bool raise = top + neg > kSlack;
     if (__any_sync(0xffffffffu, raise)) {
       float f = 1.f;
@@ -1481,7 +1481,9 @@ extern "C" QE_API int attn_decode_step(const qe_kv_cache* c, int B, int n_q, con
   const long long line = (long long)a.prefix_tiles * c->n_kv;
   a.groups = line > 0 && line < p.groups ? (int)line : p.groups;
   a.rb_prefix = p.rb_prefix; a.rb_own = p.rb_own; a.own_rows = p.own_rows;
-  a.scale_log2 = scale * kLog2e;
+  // never 0: a masked score is -inf, which stays so times any other number.  The smallest one
+  // turns scores below 2^64 into less than 2^-84, whose numerators are 1 as for a scale of 0.
+  a.scale_log2 = fmaxf(scale * kLog2e, 0x1p-149f);
   a.page = fast_div((uint32_t)c->page_size);
   a.group = fast_div((uint32_t)a.G);
   // a wide tile of two blocks of 128 rows takes about twice a narrow one's time

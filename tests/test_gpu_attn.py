@@ -290,6 +290,17 @@ def test_peaked_scores_and_page_gaps(q, cuda):
         check_attend(d, out, lse)
 
 
+@pytest.mark.parametrize("scale", [0.0, 1e-45, 2.0 ** -140], ids=["0", "smallest", "subnormal"])
+@pytest.mark.parametrize("c", [("bf16", 128, 1, 4, 16, 300, [7, 0, 130] * 15), ("f16", 64, 1, 300, 16, 0, [5, 200]),
+                               ("bf16", 256, 1, 8, 64, 70, [9] * 20), ("f16", 128, 2, 4, 16, 33, [5, 0, 64])],
+                         ids=["wide", "wide_own", "d256", "narrow"])
+def test_a_scale_of_zero_gives_the_mean(q, cuda, c, scale):
+    d = dict(attend_inputs(*c, seed=17), scale=scale)
+    out, lse, ws = run_attend(q, d)
+    assert q.qe_workspace_status(ws) == q.QE_OK
+    check_attend(d, out, lse)
+
+
 def test_strided_queries_and_outputs(q, cuda):
     import torch
     d = attend_inputs("f16", 64, 2, 2, 16, 20, [30, 5, 70], seed=3)
