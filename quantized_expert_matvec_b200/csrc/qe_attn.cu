@@ -120,6 +120,7 @@ struct AttnArgs {
   int rb_prefix, rb_own;  // row blocks per key head
   int own_rows;           // rows of an own block: min(G, kRows)
   float scale_log2;
+  float zero;             // 0, which the compiler does not know
   int run_bits;           // 2^run_bits keys lie behind one another: the power of two in page_size, at most 32; 0: no map
   FastDiv page, group;    // by the page size and by G
 };
@@ -221,6 +222,17 @@ QE_DEV u64 add_pair(u64 a, u64 b) {
   u64 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+// s - m of two products of q and k.  Their product with the scale is rounded before the
+// reference, a rounded product itself, is taken off: in one fma the largest score would keep
+// its rounding, many powers of two from scores of 2^27 on, and its numerator be infinite.
+// ptxas makes one fma of a packed product and sum, marked .rn or not, so that the product is
+// an fma of its own with two zeros that the compiler does not know (narrow blocks), or two
+// scalar products (wide ones).  128 rows behind 32768 shared keys: 196 us so, 199 us with the
+// zeros, 193 us with one fma; narrow blocks take the same time with one fma and with two.
+QE_DEV u64 exponents(u64 qk, u64 scale, u64 zero, u64 neg_ref) { return add_pair(fma_pair(qk, scale, zero), neg_ref); }
+QE_DEV u64 exponents(float qk0, float qk1, float scale, u64 neg_ref) {
+  return add_pair(pair(__fmul_rn(qk0, scale), __fmul_rn(qk1, scale)), neg_ref);
 }
 QE_DEV float exp2_approx(float x) {  // 2^-22 relative; below 2^-126: 0
   float y;
@@ -787,6 +799,7 @@ QE_DEV void soften_narrow(const AttnArgs& a, const Segment& x, int seg, int n, i
   for (int j = 0; j < J; ++j)
 #pragma unroll
     for (int e = 0; e < 16; ++e) l[j][e] = 0.f;
+  const u64 scale2 = pair(a.scale_log2, a.scale_log2), zero2 = pair(a.zero, a.zero);
   float* ref = sh.neg_ref[group];
   float* factor = sh.factor[group];
 #pragma unroll 1
@@ -812,7 +825,7 @@ QE_DEV void soften_narrow(const AttnArgs& a, const Segment& x, int seg, int n, i
           tmem_ld16(s_at + bb * 16, v);
           tmem_wait_ld(v);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = live ? v[e] * a.scale_log2 : -INFINITY;
+          for (int e = 0; e < 16; ++e) v[e] = live ? __fmul_rn(v[e], a.scale_log2) : -INFINITY;
           const float m = warp_reduce_rows_max<16>(v, lane);
           if ((lane & 1) == 0) scratch[w * kNarrow + bb * 16 + reduced_row_of_lane<16>(lane)] = m;
         }
@@ -866,10 +879,12 @@ QE_DEV void soften_narrow(const AttnArgs& a, const Segment& x, int seg, int n, i
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
             const float4 r = *reinterpret_cast<const float4*>(ref + j * 16 + e);
-            p[j][e] = fmaf(p[j][e], a.scale_log2, r.x);
-            p[j][e + 1] = fmaf(p[j][e + 1], a.scale_log2, r.y);
-            p[j][e + 2] = fmaf(p[j][e + 2], a.scale_log2, r.z);
-            p[j][e + 3] = fmaf(p[j][e + 3], a.scale_log2, r.w);
+            const float2 y0 = unpair(exponents(pair(p[j][e], p[j][e + 1]), scale2, zero2, pair(r.x, r.y)));
+            const float2 y1 = unpair(exponents(pair(p[j][e + 2], p[j][e + 3]), scale2, zero2, pair(r.z, r.w)));
+            p[j][e] = y0.x;
+            p[j][e + 1] = y0.y;
+            p[j][e + 2] = y1.x;
+            p[j][e + 3] = y1.y;
           }
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -978,7 +993,7 @@ QE_DEV void soften_wide(const AttnArgs& a, const Segment& x, int seg, int n, int
         for (int e = 0; e < 16; e += 2) t[(e >> 1) & 3] = fmaxf(t[(e >> 1) & 3], fmaxf(v[k][e], v[k][e + 1]));
       top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
     }
-    top *= a.scale_log2;  // scale > 0
+    top = __fmul_rn(top, a.scale_log2);  // scale > 0
     const bool raise = top + neg > kSlack;
     if (__any_sync(0xffffffffu, raise)) {
       float f = 1.f;
@@ -1004,7 +1019,7 @@ QE_DEV void soften_wide(const AttnArgs& a, const Segment& x, int seg, int n, int
     }
     // (a masked score is -inf and its numerator 0, unless nothing was ever seen: neg is
     // 3e38 then, and -inf + 3e38 is -inf still)
-    const u64 scale2 = pair(a.scale_log2, a.scale_log2), neg2 = pair(neg, neg);
+    const u64 neg2 = pair(neg, neg);
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
       half_row(c);
@@ -1014,7 +1029,7 @@ QE_DEV void soften_wide(const AttnArgs& a, const Segment& x, int seg, int n, int
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           float* x = &v[2 * k + (e >> 4)][e & 15];
-          const float2 y = unpair(fma_pair(pair(x[0], x[1]), scale2, neg2));
+          const float2 y = unpair(exponents(x[0], x[1], a.scale_log2, neg2));
           const float x0 = exp2_approx(y.x), x1 = exp2_approx(y.y);
           sum[(e >> 1) & 1] = add_pair(sum[(e >> 1) & 1], pair(x0, x1));
           pk[e >> 1] = pack2<T>(x0, x1);

@@ -301,6 +301,36 @@ def test_a_scale_of_zero_gives_the_mean(q, cuda, c, scale):
     check_attend(d, out, lse)
 
 
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 19 / 3, 1e9, 2.0 ** 64], ids=["1", "2e5", "1e9", "2^64"])
+@pytest.mark.parametrize("dtype,D,B,G,prefix,n", [("f16", 128, 70, 4, 300, 40), ("bf16", 64, 2, 4, 0, 700),
+                                                  ("f16", 256, 3, 2, 130, 5), ("bf16", 256, 40, 4, 300, 9)])
+def test_scores_beyond_the_mantissa(q, cuda, dtype, D, B, G, prefix, n, scale):
+    """Whole numbers as q and k: their products' sums are exact, and two sums differ by 1 at
+    least.  From a scale of 1e5 on every weight but the largest sum's is 0: out is the mean of
+    the values that have it."""
+    import torch
+    d = attend_inputs(dtype, D, 1, G, 16, prefix, [n] * B, seed=18)
+    g = torch.Generator(device="cuda").manual_seed(19)
+    for name in ("kp", "vp"):
+        d[name] = torch.randint(-9, 10, d[name].shape, generator=g, device="cuda").to(dt(dtype))
+    d["q"] = torch.randint(-9, 10, d["q"].shape, generator=g, device="cuda").to(dt(dtype))
+    d["scale"] = scale
+    out, lse, _ = run_attend(q, d)
+    if scale == 1.0:
+        return check_attend(d, out, lse)
+    kp, vp, qq, out, lse = (host(x) for x in (d["kp"], d["vp"], d["q"], out, lse))
+    for b in range(B):
+        k, v = (np.concatenate([ref.gather(p, 16, d["pp"], prefix, 0), ref.gather(p, 16, d["tb"][b], n, 0)]) for p in (kp, vp))
+        s = qq[b] @ k.T
+        best = s == s.max(axis=1, keepdims=True)
+        want = (best @ v) / best.sum(axis=1, keepdims=True)
+        # l and the sums of values are small whole numbers; 1 / l, the product and the result are rounded
+        assert np.all(np.abs(out[b] - want) <= (ref.HALF_STEP[dtype] + 2.0 ** -22) * np.abs(want))
+        # scale log2(e), its product with the score, the logarithm's sum and the product with ln 2
+        want = np.float64(np.float32(scale)) * s.max(axis=1) + np.log(best.sum(axis=1))
+        assert np.all(np.abs(lse[b] - want) <= 6 * ref.U32 * np.abs(want))
+
+
 def test_strided_queries_and_outputs(q, cuda):
     import torch
     d = attend_inputs("f16", 64, 2, 2, 16, 20, [30, 5, 70], seed=3)
