@@ -41,10 +41,10 @@
 // copies each of these stays within a tenth: what bounds a tile is the hand-over from one
 // role to the next (producers, scores, softmax, outputs), it seems: about 2.4 us a wide tile and
 // 1.3 us a narrow one, and 8 us before the first.
-// The reference m need not be the maximum: it is raised (and o, l rescaled) only
-// when a score passes it by more than 2^8.  l is the sum of the fp32 numerators;
-// their rounding to the cache's dtype is the one that the second product's
-// operand type asks for.
+// The reference m need not be the maximum (for fp16 it is set 7 below it): it is raised,
+// and o and l rescaled, only when a score passes the maximum that it was set by by more
+// than 2^8.  l is the sum of the fp32 numerators; their rounding to the cache's dtype is
+// the one that the second product's operand type asks for.
 #include <cuda.h>  // types of the tensor map
 #include <cuda_runtime.h>
 #include <math.h>
@@ -65,7 +65,13 @@ constexpr int kTile = 128;       // keys per tile
 constexpr int kNarrow = 64;      // most rows of a narrow block
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNoRef = 3.0e38f;  // -m before the first score
-constexpr float kSlack = 8.f;      // a score may pass the reference by this (log2)
+constexpr float kSlack = 8.f;      // a score may pass the one that set the reference by this (log2)
+// The reference is this far below the largest score (log2).  fp16 numerators below 2^-25 become
+// 0, and l counts them all the same: 60000 keys at 2^-25.5 of the largest are a thousandth of
+// the mass.  Seven powers of two and the slack make 2^15, which fp16 still holds.  bf16 has
+// fp32's exponents.
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;
 // A segment costs its CTA about one tile's time beside its tiles (queries, first
 // reference, results): the deal counts that in.
 constexpr int kSegmentCost = 1;
@@ -833,7 +839,7 @@ QE_DEV void soften_narrow(const AttnArgs& a, const Segment& x, int seg, int n, i
         if (key < nb * 16) {
           const float old = i == 0 ? -kNoRef : -ref[key];
           const float m = fmaxf(fmaxf(fmaxf(scratch[key], scratch[kNarrow + key]),
-                                      fmaxf(scratch[2 * kNarrow + key], scratch[3 * kNarrow + key])), old);
+                                      fmaxf(scratch[2 * kNarrow + key], scratch[3 * kNarrow + key])) - kLift<T>, old);
           ref[key] = -m;
           factor[key] = exp2_approx(old - m);
         }
@@ -895,7 +901,7 @@ QE_DEV void soften_narrow(const AttnArgs& a, const Segment& x, int seg, int n, i
           }
           most = fmaxf(most, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
         }
-      if (raise || !group_vote(group, most > kSlack)) break;
+      if (raise || !group_vote(group, most > kSlack + kLift<T>)) break;
     }
     unsigned char* p_row = ps + (n & 1) * Sh::kP + key * 128;
 #pragma unroll
@@ -994,7 +1000,8 @@ QE_DEV void soften_wide(const AttnArgs& a, const Segment& x, int seg, int n, int
       top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
     }
     top = __fmul_rn(top, a.scale_log2);  // scale > 0
-    const bool raise = top + neg > kSlack;
+    const bool raise = top + neg > kSlack + kLift<T>;
+    top -= kLift<T>;
     if (__any_sync(0xffffffffu, raise)) {
       float f = 1.f;
       if (raise) {

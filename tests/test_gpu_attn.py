@@ -331,6 +331,37 @@ def test_scores_beyond_the_mantissa(q, cuda, dtype, D, B, G, prefix, n, scale):
         assert np.all(np.abs(lse[b] - want) <= 6 * ref.U32 * np.abs(want))
 
 
+@pytest.mark.parametrize("G,prefix,n", [(1, 0, 60000), (64, 30000, 0)], ids=["own_keys", "prefix"])
+def test_fp16_keeps_the_tail_of_long_rows(q, cuda, G, prefix, n):
+    """One key of weight 1 and value 0, all others of weight 2^-25.5 and value 1000, in segments that
+    begin with the one: fp16 numerators that have 2^0 for the largest would lose every other."""
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    B = sms if not prefix else 4 * sms  # a row of own keys, or a block of 256 prefix rows, for each multiprocessor
+    d = attend_inputs("f16", 64, 1, G, 64, prefix, [n], seed=20)
+    d["B"], d["lens"], d["tb"] = B, [n] * B, np.repeat(d["tb"], B, axis=0)
+    d["q"] = torch.zeros((B, G, 64), dtype=torch.float16, device="cuda")
+    d["q"][:, :, 3] = 1.0
+    tail = -17.6875
+    d["kp"][:, :, :, :] = 0.0
+    d["kp"][:, :, :, 3] = tail
+    d["vp"][:, :, :, :] = 1000.0
+    at = (d["pp"] if prefix else d["tb"][0])[0]
+    d["kp"][at, 0, 0, 3], d["vp"][at, 0, 0] = 0.0, 0.0
+    d["scale"] = 1.0
+    out, lse, _ = run_attend(q, d)
+    keys = prefix + n
+    w = math.exp(tail)
+    total = 1 + (keys - 1) * w
+    want = 1000.0 * (keys - 1) * w / total
+    # a numerator is off by 2^-25 (half of fp16's smallest) where the largest is 2^7, the sums by
+    # their terms' roundings, the result by half a step
+    tol = 1000.0 * keys * 2.0 ** -32 / total + (keys + 64) * 2 * ref.U32 * want + ref.HALF_STEP["f16"] * want
+    assert tol < want / 20
+    assert np.abs(host(out) - want).max() <= tol
+    assert np.abs(host(lse) - math.log(total)).max() <= (keys + 64) * 2 * ref.U32 + 2.0 ** -21
+
+
 def test_strided_queries_and_outputs(q, cuda):
     import torch
     d = attend_inputs("f16", 64, 2, 2, 16, 20, [30, 5, 70], seed=3)
