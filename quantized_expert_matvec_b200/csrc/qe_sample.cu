@@ -66,6 +66,11 @@ constexpr int kAhead = 2;   // STREAM: 16-byte pieces a thread has on their way
 constexpr int kGroups = 4;  // groups of a thread's logits of which the largest is kept
 constexpr int kMaxVocab = 1 << 19;
 constexpr int kMaxCluster = 16;
+// Logits of one CTA.  The histogram adds 16-bit pieces of the weights in 32-bit words:
+// 2^16 of them in one bin make less than 2^32.
+constexpr int kMaxRun = 1 << 16;
+constexpr int kRowBytes = 72 * 1024;  // of a CTA's run in shared memory, while more CTAs a row can be had
+static_assert(kRowBytes / 2 <= kMaxRun && kMaxVocab / kMaxCluster <= kMaxRun, "runs on chip");
 
 struct SampleArgs {
   const void* logits;
@@ -1017,12 +1022,14 @@ cudaError_t launch_sample_t(SampleArgs a, cudaStream_t s) {
   const int es = (int)sizeof(T);
   const int at_once = 2 * dev_info().sms;
   int cl = 1;
-  while (cl < 16 && (long long)a.V * es / cl > 72 * 1024) cl *= 2;
+  while (cl < 16 && (long long)a.V * es / cl > kRowBytes) cl *= 2;
   while (cl < 16 && (long long)a.V * es / cl > 8 * 1024 && (long long)a.B * cl * 2 <= at_once) cl *= 2;
   const int n = 16 / es;
   if (cl > 1 && (long long)a.B * cl > 2ll * at_once) {  // clusters in more than two waves
-    a.cluster = kStreamCluster;
-    a.run = ((a.V + a.cluster - 1) / a.cluster + n - 1) / n * n;
+    for (a.cluster = kStreamCluster;; a.cluster *= 2) {  // eight for more than 4 kMaxRun logits
+      a.run = ((a.V + a.cluster - 1) / a.cluster + n - 1) / n * n;
+      if (a.run <= kMaxRun) break;
+    }
     a.smem_row = 0;
     return launch_sample_as<T, true>(a, s);
   }

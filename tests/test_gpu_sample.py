@@ -214,6 +214,34 @@ def test_many_large_rows(q, cuda, dtype, V, pad):
     assert np.array_equal(t, token[few]) and np.array_equal(l, lp[few])
 
 
+def test_streamed_rows_of_the_largest_vocabulary(q, cuda):
+    # so many rows of 524288 logits that they are read in passes, most logits of a row in one
+    # bin of the histogram: sums over more logits than 32 bits hold for 16-bit pieces of the weights
+    import torch
+    B, V = 40, 524288
+    g = torch.Generator(device="cuda").manual_seed(21)
+    x = torch.empty((B, V), device="cuda")
+    kw = dict(temperature=[1.0] * B, top_p=[0.0] * B)
+    for b in range(B):
+        x[b] = -0.01 - 0.037 * b                                     # one value: bins 0 .. a few hundred
+        kw["top_p"][b] = 0.3 + 0.69 * (b * 0.618 % 1)
+        if b % 4 == 1:
+            x[b] += 0.05 * torch.rand(V, generator=g, device="cuda")  # near one another
+        elif b % 4 == 2:
+            x[b] = -40.0 - 10 * torch.rand(V, generator=g, device="cuda")  # the last bin
+            kw["temperature"][b] = 60.0
+        x[b, (1009 * b + 7) % V] = 0.1
+    x[3] = torch.where(torch.rand(V, generator=g, device="cuda") < 0.4, -math.inf, x[3])
+    for keep in (None, [int(V * (0.2 + 0.019 * b)) for b in range(B)]):
+        kk = dict(kw, top_k=keep) if keep else kw
+        u = np.random.RandomState(22).rand(B).astype(np.float32)
+        token, lp = run(q, x, u, **kk)
+        check(x, u, token, lp, **kk)
+        few = slice(18, 20)  # kept on chip: the same tokens
+        t, l = run(q, x[few].clone(), u[few], **{n: v[few] for n, v in kk.items()})
+        assert np.array_equal(t, token[few]) and np.array_equal(l, lp[few])
+
+
 def test_outputs_beside_the_batch_stay(q, cuda):
     import torch
     x = rows(4, 777, "f32", 10)
