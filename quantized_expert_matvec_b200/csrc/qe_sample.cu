@@ -798,7 +798,9 @@ QE_DEV void choose(Row<T, STREAM>& r, float best, const float (&group)[kGroups],
       uint32_t k_min = (uint32_t)bounds[0];
       for (uint32_t c = 1; c < r.size; ++c) k_min = min(k_min, (uint32_t)bounds[c]);
       // a lowest logit as a bound on the difference (which rounds the same way for both)
-      if (k_min > key_of(-INFINITY)) far = __uint_as_float(__float_as_uint(r.x_max - logit_of(k_min)) + 1);
+      // (a difference beyond fp32 bounds nothing)
+      const float d = r.x_max - logit_of(k_min);
+      if (k_min > key_of(-INFINITY) && d < INFINITY) far = __uint_as_float(__float_as_uint(d) + 1);
     }
   } else if (cut_p) {
     r.hist_clear();
@@ -819,7 +821,9 @@ QE_DEV void choose(Row<T, STREAM>& r, float best, const float (&group)[kGroups],
     far = fminf(far, __double2float_ru(d * (1.0 + 1e-6) + 1e-37));
   }
   if (INF) far = 0.f;  // only its equals, whose difference is no number
-  if (far < INFINITY || a.V <= kMaxCand) {
+  // without a bound: all but -inf, by their differences, which are finite below 2^100 (the
+  // others' may not be; a test of x itself costs every row 3%)
+  if (far < INFINITY || (a.V <= kMaxCand && r.x_max < 0x1p100f)) {
     auto near = [&](float x) { return INF ? x == INFINITY : r.x_max - x < far; };
     const u64 n = r.running([&](float x, int) -> u64 { return near(x) ? 1 : 0; }, &mine, &before);
     if (n <= kMaxCand) {

@@ -242,6 +242,27 @@ def test_streamed_rows_of_the_largest_vocabulary(q, cuda):
         assert np.array_equal(t, token[few]) and np.array_equal(l, lp[few])
 
 
+@pytest.mark.parametrize("V", [2, 900, 2048, 2049, 5000])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_differences_beyond_the_type(q, cuda, V, dtype):
+    # a token forced by the type's largest value over masks of its lowest: their difference is infinite
+    import torch
+    top, low = torch.finfo(dt(dtype)).max, torch.finfo(dt(dtype)).min
+    x = torch.full((8, V), low, device="cuda").to(dt(dtype))
+    for b in range(8):
+        x[b, (b * 37 + 1) % V] = top
+    x[5:, V // 2:] = -math.inf
+    x[6, 0] = 3.0
+    for kw in (dict(), dict(top_k=[1, 2, 3, 50, V - 1, 7, 2, 2]), dict(top_k=[2] * 8, top_p=[0.9] * 8), dict(top_p=[0.5] * 8),
+               dict(min_p=[0.1] * 8), dict(top_k=[3] * 8, min_p=[0.5] * 8),
+               dict(temperature=[math.inf, 1e38, 2e38, 3e38, 1e37, 1e38, math.inf, 1e38]),
+               dict(temperature=[math.inf, 1e38, 2e38, 3e38, 1e37, 1e38, math.inf, 1e38], top_k=[2] * 8)):
+        for s in range(3):
+            u = np.random.RandomState(s).rand(8).astype(np.float32)
+            token, lp = run(q, x, u, **kw)
+            check(x, u, token, lp, **kw)
+
+
 def test_outputs_beside_the_batch_stay(q, cuda):
     import torch
     x = rows(4, 777, "f32", 10)
