@@ -443,8 +443,8 @@ typedef struct {
  * call, NULL = axis 0 for all) says which of the n_axes positions of a token
  * (1 to 4: one for text; time, height and width for images and video) turns
  * pair i, in any order.  rotary_dim is a multiple of 16 and at most head_dim.
- * inv_freq fp32 [rotary_dim / 2] device.  The angle is formed and reduced in
- * fp64, so far positions keep fp32 accuracy. */
+ * inv_freq fp32 [rotary_dim / 2] device.  The angle's product is exact and it is
+ * reduced in fp64, so far positions keep fp32 accuracy (angles below 2^45). */
 typedef struct {
   const float* inv_freq;
   const uint8_t* pair_axis;

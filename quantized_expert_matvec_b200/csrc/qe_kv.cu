@@ -48,16 +48,17 @@ struct KvArgs {
   uint8_t axis[kMaxPairs];
 };
 
-// sin and cos of the angle a = pos * f.  The product of an integer below 2^31
-// and an fp32 number is exact in fp64; the nearest multiple of pi / 2 is taken
-// off in two parts (pi / 2 to 106 bits), which leaves |r| <= pi / 4 to about
-// 2^-52 (n up to 2^31).  On that interval the Taylor polynomials to r^9 and r^10 are
-// off by at most r^11 / 11! = 1.8e-9 and r^12 / 12! = 1.2e-10, below fp32's half step.
+// sin and cos of the angle pos * f.  The product of an integer below 2^31 and an fp32
+// number has up to 55 bits: a is the nearest fp64 number and `rest` what it lacks, exactly.
+// The nearest multiple of pi / 2 is taken off a in two parts (Cody and Waite's reduction,
+// pi / 2 to 106 bits), which leaves |r| <= pi / 4 + 2^-8 to about 2^-52 for angles up to
+// 2^45.  On that interval the Taylor polynomials to r^9 and r^10 are off by at most
+// r^11 / 11! = 1.9e-9 and r^12 / 12! = 1.3e-10, below fp32's half step.
 QE_DEV float2 cos_sin(int pos, float f) {
-  const double a = (double)pos * (double)f;
+  const double a = (double)pos * (double)f, rest = fma((double)pos, (double)f, -a);
   const double n = rint(a * 0.63661977236758134308);
   double rd = fma(-n, 1.5707963267948965580, a);
-  rd = fma(-n, 6.1232339957367660359e-17, rd);
+  rd = fma(-n, 6.1232339957367660359e-17, rd) + rest;
   const int quadrant = (int)(__double2ll_rn(n) & 3);
   const float r = (float)rd, z = r * r;
   float s = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);

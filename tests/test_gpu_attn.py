@@ -117,6 +117,39 @@ def test_append_matches_the_definition(q, cuda, c):
     check_append(c, d)
 
 
+def exact_angle(pos, f):
+    """pos * f reduced by the nearest multiple of 2 pi, from whole numbers (f is an fp32 number)."""
+    from fractions import Fraction
+    two_pi = Fraction(2 * 31415926535897932384626433832795028841971693993751058209749445923, 10 ** 64)
+    a = Fraction(int(pos)) * Fraction(float(f))
+    return float(a - round(a / two_pi) * two_pi)
+
+
+def test_angles_of_far_positions(q, cuda):
+    # positions and frequencies whose product has more bits than fp64: q is a unit vector, so that
+    # q_out is cosine and sine themselves
+    import torch
+    rng = np.random.RandomState(23)
+    T, D = 200, 64
+    half = D // 2
+    pos = np.concatenate([rng.randint(2 ** 30, 2 ** 31 - 1, T - 3), [2 ** 31 - 1, 2 ** 30 + 1, 1]]).astype(np.int32)
+    f = np.concatenate([rng.uniform(0.5, 1.0, half // 2), np.exp(rng.uniform(0, math.log(16000), half // 2))]).astype(np.float32)
+    x = torch.zeros((T, 1, D), device="cuda")
+    x[:, :, :half] = 1.0
+    kp = torch.zeros((T, 1, 8, D), dtype=torch.float16, device="cuda")
+    kc = q.KVCache(kp, torch.zeros_like(kp))
+    out = torch.zeros((T, 1, D), dtype=torch.float16, device="cuda")
+    table = torch.arange(T, dtype=torch.int32, device="cuda").reshape(T, 1)
+    ws = q.attn_workspace(kc, 1, 1)
+    q.attn_kv_append(kc, x, x, x, table, torch.zeros(T, dtype=torch.int32, device="cuda"), out,
+                     rope=q.Rope(torch.from_numpy(f).cuda()), pos=torch.from_numpy(pos).cuda().reshape(1, T), ws=ws)
+    angle = np.array([[exact_angle(p, y) for y in f] for p in pos])
+    want = np.concatenate([np.cos(angle), np.sin(angle)], axis=1)
+    e = 2.0 ** -23 + 2 * ref.U32  # as in check_append, |a| + |b| = 1
+    for got in (host(out)[:, 0], host(kp)[:, 0, 0]):
+        assert np.all(np.abs(got - want) <= e + ref.HALF_STEP["f16"] * (np.abs(want) + e) + ref.TINY["f16"])
+
+
 def test_append_without_rotation_copies_bits(q, cuda):
     # no rope: q_out and the cache hold the inputs' bits, infinities and NaN too; seq None is the token's number
     import torch
