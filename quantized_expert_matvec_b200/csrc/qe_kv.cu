@@ -172,12 +172,13 @@ __global__ void __launch_bounds__(kKvThreads) qe_kv_append_kernel(const __grid_c
       dst = (TC*)(is_k ? a.kc : a.vc) + (long long)page * (is_k ? a.k_page_stride : a.v_page_stride) +
             ((long long)h * a.page.d + off) * a.D;
     }
+    bool second = true;
     if constexpr (sizeof(TI) == 2 && std::is_same<TI, TC>::value) {
-      if (!x.turn) {  // the bits as they are (a NaN's too)
-        *reinterpret_cast<uint4*>(dst + x.e0) = x.r0.a;
-        *reinterpret_cast<uint4*>(dst + x.e1) = x.r1.a;
-        return;
-      }
+      // what is not turned: the bits as they are (a NaN's too)
+      if (!x.turn) *reinterpret_cast<uint4*>(dst + x.e0) = x.r0.a;
+      second = x.turn && !(ADJ && x.e1 >= a.rd);
+      if (!second) *reinterpret_cast<uint4*>(dst + x.e1) = x.r1.a;
+      if (!x.turn) return;
     }
     float u[8], v[8];
     x.r0.get(u);
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kKvThreads) qe_kv_append_kernel(const __grid_c
       }
     }
     store8(dst + x.e0, u);
-    store8(dst + x.e1, v);
+    if (second) store8(dst + x.e1, v);
   };
 
   // the first items are on their way while places and angles are worked out

@@ -183,6 +183,30 @@ def test_append_without_rotation_copies_bits(q, cuda):
     assert q.qe_workspace_status(ws) == q.QE_OK
 
 
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_elements_past_the_rotation_keep_their_bits(q, cuda, adjacent, dtype):
+    # every rotary_dim of a head: what lies behind it is copied, with a NaN's payload
+    import torch
+    T, D = 2, 128
+    kp = torch.zeros((T, 1, 8, D), dtype=dt(dtype), device="cuda")
+    kc = q.KVCache(kp, torch.zeros_like(kp))
+    ws = q.attn_workspace(kc, 1, 1)
+    table = torch.arange(T, dtype=torch.int32, device="cuda").reshape(T, 1)
+    at = torch.zeros(T, dtype=torch.int32, device="cuda")
+    exponent = {"f16": 0x7c00, "bf16": 0x7f80}[dtype]
+    bits = torch.arange(T * D, device="cuda").remainder(60).add(1 + exponent).to(torch.int16)
+    x = torch.where(torch.arange(T * D, device="cuda") % 2 == 0, bits, bits - 32768).to(torch.int16).view(dt(dtype)).reshape(T, 1, D)
+    assert bool(x.isnan().all())
+    for rd in range(0, D + 1, 16):
+        out = torch.zeros((T, 1, D), dtype=dt(dtype), device="cuda")
+        rope = q.Rope(torch.rand(rd // 2, device="cuda"), adjacent=adjacent)
+        q.attn_kv_append(kc, x, x, x, table, at, out, rope=rope, ws=ws)
+        for got in (out[:, :, rd:], kp[:, :, 0, rd:]):
+            assert torch.equal(got.contiguous().view(torch.int16), x[:, :, rd:].contiguous().view(torch.int16)), rd
+        assert bool(out[:, :, :rd].isnan().all())
+
+
 def test_append_records_bad_places_and_writes_nothing_there(q, cuda):
     import torch
     T, D, page = 5, 64, 8
