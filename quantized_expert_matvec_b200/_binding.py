@@ -449,6 +449,11 @@ def _heads(name, t, dtype, T, heads, dim, dev):
     return t.data_ptr(), s[0]
 
 
+def _need(name, t):
+    if t is None:
+        raise ValueError(f"{name} is missing")
+
+
 def _on(stream, dev):
     return _raw_stream(dev) if stream is None else _stream(stream)
 
@@ -525,7 +530,11 @@ def attn_kv_append(cache: KVCache, q, k, v, table, kv_pos, q_out=None, rope: Rop
     to the cache, token t at place kv_pos[t] (int32; negative: padding) of the
     sequence whose pages are table[seq[t]] (int32 [n_seq, columns]; seq None:
     t).  pos int32 [n_axes, T] are the rotation's positions (None: kv_pos).  q may
-    be None; q_out may be q itself where the dtypes agree."""
+    be None, else q_out is needed; q_out may be q itself where the dtypes agree.
+    ws: any workspace."""
+    _need("ws", ws)
+    if q is not None:
+        _need("q_out", q_out)
     dev, D, dtype = _device(), cache.head_dim, k.dtype
     i32, T, n_kv = _torch.int32, k.shape[0], cache.n_kv
     if cache._dev != dev:
@@ -557,7 +566,9 @@ def attn_decode_step(cache: KVCache, q, out, table, kv_len, prefix_pages=None, p
     prefix_pages (int32), shared by all rows, and each row's kv_len[b] own
     tokens on table[b] (int32 [B, columns]; kv_len negative: a padding row, left
     as it was), into out.  scale defaults to head_dim ** -0.5; lse float32
-    [B, n_q] receives the logarithm of the softmax's denominator."""
+    [B, n_q] receives the logarithm of the softmax's denominator; ws is
+    attn_workspace's."""
+    _need("ws", ws)
     dev, D, dtype = _device(), cache.head_dim, cache.dtype
     i32 = _torch.int32
     B, n_q = q.shape[0], q.shape[1]

@@ -133,6 +133,18 @@ def test_binding_checks_before_the_library(q):
         q.Rope(torch.zeros(8))
 
 
+def test_binding_names_what_is_missing(q):
+    # the arguments with a default of None that a call cannot do without
+    import torch
+    t = torch.zeros((2, 2, 64))
+    with pytest.raises(ValueError, match="ws is missing"):
+        q.attn_kv_append(None, t, t, t, t, t, t)
+    with pytest.raises(ValueError, match="q_out is missing"):
+        q.attn_kv_append(None, t, t, t, t, t, ws=t)
+    with pytest.raises(ValueError, match="ws is missing"):
+        q.attn_decode_step(None, t, t, t, t)
+
+
 def test_reference_rotation_is_a_rotation():
     # lengths of the pairs stay, a quarter turn swaps them, no pair beyond rotary_dim moves
     rng = np.random.RandomState(0)
