@@ -461,7 +461,8 @@ typedef struct {
  *     multiple of 8; all 16-byte aligned.  q may be NULL with n_q = 0.
  *   q_out [T][n_q][head_dim] device, the cache's dtype, q_out_stride as above.
  *     It may be q itself (same dtype and stride); otherwise it must not
- *     overlap q, k or v.
+ *     overlap q, and in no case k or v.  Places of its own in the same rows
+ *     (one buffer, one stride in bytes) do not overlap.
  *   rope NULL: nothing is rotated (q_out is q in the cache's dtype).
  *   pos int32 [n_axes][T] device: positions for the rotation, NULL = kv_pos on
  *     every axis.
@@ -493,8 +494,8 @@ QE_API size_t attn_workspace_bytes(const qe_kv_cache* cache, int n_q, int B);
  * kv_len[b] tokens of the pages table[b][0 ..]; head i reads key head
  * i / (n_q / n_kv).  The prefix is read once for the whole batch.
  *   q, out [B][n_q][head_dim] device, the cache's dtype, 16-byte aligned, not
- *     overlapping; q_stride, out_stride: elements from row to row, a multiple
- *     of 8.
+ *     overlapping (places of their own in the same rows do not); q_stride,
+ *     out_stride: elements from row to row, a multiple of 8.
  *   prefix_pages int32 device [ceil(prefix_len / page_size)], NULL with
  *     prefix_len = 0.  prefix_len is a host value (a captured graph keeps it).
  *   kv_len int32 [B] device; table int32 [B][table_stride] device.  kv_len 0:

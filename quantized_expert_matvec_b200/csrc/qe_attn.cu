@@ -1477,8 +1477,8 @@ extern "C" QE_API int attn_decode_step(const qe_kv_cache* c, int B, int n_q, con
   if ((q_stride | out_stride) & 7) return fail(QE_ERR_INVALID_ARG, "row strides must be multiples of 8 elements");
   if (B > 1 && (q_stride < (int64_t)n_q * D || out_stride < (int64_t)n_q * D))
     return fail(QE_ERR_INVALID_ARG, "row strides must cover a row's heads");
-  const size_t last = (size_t)B - 1;
-  if (ranges_overlap(out, 2 * (last * out_stride + (size_t)n_q * D), q, 2 * (last * q_stride + (size_t)n_q * D)))
+  const size_t row = 2 * (size_t)n_q * D;
+  if (rows_overlap({out, row, 2 * (size_t)out_stride, B}, {q, row, 2 * (size_t)q_stride, B}))
     return fail(QE_ERR_INVALID_ARG, "out overlaps q");
   if (!ws || ((uintptr_t)ws & 255)) return fail(QE_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
   const int sms = dev_info().sms;

@@ -52,6 +52,12 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
 }
 
 int check_kv_cache(const qe_kv_cache* c);
-bool ranges_overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes);
+// n rows of `row` bytes, `stride` bytes apart
+struct Rows {
+  const void* p;
+  size_t row, stride;
+  int n;
+};
+bool rows_overlap(const Rows& a, const Rows& b);  // a.n == b.n
 
 }  // namespace qe

@@ -289,9 +289,15 @@ int check_kv_cache(const qe_kv_cache* c) {
   return QE_OK;
 }
 
-bool ranges_overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
-  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-  return a0 < b0 + b_bytes && b0 < a0 + a_bytes;
+// Between the first and the last row of both, rows the same distance apart overlap where their
+// places within that distance do; others, which may meet somewhere, count as overlapping.
+bool rows_overlap(const Rows& a, const Rows& b) {
+  const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+  const size_t last = (size_t)a.n - 1, a1 = a0 + last * a.stride + a.row, b1 = b0 + last * b.stride + b.row;
+  if (a0 >= b1 || b0 >= a1) return false;
+  if (a.n == 1 || a.stride != b.stride) return true;
+  const size_t d = b0 >= a0 ? (b0 - a0) % a.stride : (a.stride - (a0 - b0) % a.stride) % a.stride;
+  return d < a.row || d + b.row > a.stride;
 }
 
 }  // namespace qe
@@ -332,12 +338,12 @@ extern "C" QE_API int attn_kv_append(const qe_kv_cache* c, const qe_rope* rope, 
     return fail(QE_ERR_INVALID_ARG, "token strides must cover a token's heads");
   if (!ws || ((uintptr_t)ws & 255) || ws_bytes < sizeof(WsControl))
     return fail(QE_ERR_INVALID_ARG, "workspace must be 256-byte aligned and hold its control block");
-  if (n_q > 0 && !(q_out == q && q_out_stride == q_stride && in_dtype == c->dtype)) {
-    const size_t es = in_dtype == QE_F32 ? 4 : 2, last = (size_t)T - 1;
-    const size_t ob = 2 * (last * q_out_stride + (size_t)n_q * D);
-    if (ranges_overlap(q_out, ob, q, es * (last * q_stride + (size_t)n_q * D)) ||
-        ranges_overlap(q_out, ob, k, es * (last * k_stride + (size_t)c->n_kv * D)) ||
-        ranges_overlap(q_out, ob, v, es * (last * v_stride + (size_t)c->n_kv * D)))
+  if (n_q > 0) {
+    const size_t es = in_dtype == QE_F32 ? 4 : 2, q_row = (size_t)n_q * D, kv_row = (size_t)c->n_kv * D;
+    const bool in_place = q_out == q && (q_out_stride == q_stride || T == 1) && in_dtype == c->dtype;
+    const Rows to{q_out, 2 * q_row, 2 * (size_t)q_out_stride, T};
+    if ((!in_place && rows_overlap(to, {q, es * q_row, es * (size_t)q_stride, T})) ||
+        rows_overlap(to, {k, es * kv_row, es * (size_t)k_stride, T}) || rows_overlap(to, {v, es * kv_row, es * (size_t)v_stride, T}))
       return fail(QE_ERR_INVALID_ARG, "q_out overlaps q, k or v");
   }
   KvArgs a{};

@@ -84,6 +84,27 @@ def test_append_refuses_rotations(q, kw, what):
     assert what in q.qe_last_error()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(out=16 * M, kp=16 * M, ks=512),                                         # in place: k is q's first heads
+    dict(out=16 * M, vp=16 * M + 512, vs=512),                                   # v its last ones
+    dict(out=16 * M, kp=16 * M + 1024, ks=512),                                  # the next token's
+    dict(out=16 * M, qs=1024, os=1024, kp=16 * M + 1792, ks=1024),               # k runs into the next token's q
+    dict(out=16 * M, qs=1024, os=1024, vp=16 * M + 1024, vs=1032),               # another stride: they meet somewhere
+    dict(out=16 * M + 1024, qs=1024, os=1024, kp=16 * M + 1536, ks=1024),        # k in a q_out beside q
+    dict(T=1, out=16 * M, kp=16 * M + 768, ks=512),
+])
+def test_append_refuses_inputs_that_it_would_overwrite(q, kw):
+    assert append(q, **kw) == q.QE_ERR_INVALID_ARG
+    assert "overlaps" in q.qe_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(qs=1024, os=1024, out=16 * M + 1008), dict(qs=1024, os=1024, out=16 * M + 1040),
+                                dict(qs=1024, os=1032, out=16 * M + 1024), dict(qs=1024, os=1024, out=16 * M - 1008)])
+def test_attention_refuses_outputs_on_queries(q, kw):
+    assert attend(q, **kw) == q.QE_ERR_INVALID_ARG
+    assert "overlaps" in q.qe_last_error()
+
+
 @pytest.mark.parametrize("kw,what", [
     (dict(n_q=3), "n_q"), (dict(n_q=0), "n_q"), (dict(B=-1), "B must"), (dict(B=4097), "B must"),
     (dict(prefix_len=-1), "prefix_len"), (dict(prefix_len=1 << 30), "prefix_len"), (dict(prefix_len=5), "prefix_pages"),

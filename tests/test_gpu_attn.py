@@ -432,6 +432,39 @@ def test_strided_queries_and_outputs(q, cuda):
     assert bool((into[:, :4] == 0).all()) and bool((into[:, 8:] == 0).all())
 
 
+def test_places_of_the_same_rows(q, cuda):
+    # q, k, v, q_out and the attention's out as slices of one buffer's rows; q in place beside k and v
+    import torch
+    T, n_q, n_kv, D, page = 9, 4, 2, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(24)
+    first = torch.randn((T, 3 * n_q + 2 * n_kv, D), generator=g, device="cuda").to(torch.bfloat16)
+    kp = torch.zeros((T, n_kv, page, D), dtype=torch.bfloat16, device="cuda")
+    kc = q.KVCache(kp, torch.zeros_like(kp))
+    ws = q.attn_workspace(kc, n_q, T)
+    table = torch.arange(T, dtype=torch.int32, device="cuda").reshape(T, 1)
+    at = torch.zeros(T, dtype=torch.int32, device="cuda")
+    rope = q.Rope(torch.rand(D // 2, generator=g, device="cuda"))
+    pos = torch.arange(5, 5 + T, dtype=torch.int32, device="cuda")
+
+    def step(x, to, out):
+        q.attn_kv_append(kc, x[:, :n_q], x[:, n_q:n_q + n_kv], x[:, n_q + n_kv:n_q + 2 * n_kv], table, at, to, rope=rope,
+                         pos=pos, ws=ws)
+        q.attn_decode_step(kc, to, out, table, at + 1, ws=ws)
+        return to.clone(), out.clone(), kp.clone()
+
+    new = torch.zeros((2, T, n_q, D), dtype=torch.bfloat16, device="cuda")
+    want = step(first, new[0], new[1])
+    x = first.clone()
+    got = step(x, x[:, -n_q:], x[:, n_q + 2 * n_kv:-n_q])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(x[:, :n_q + 2 * n_kv], first[:, :n_q + 2 * n_kv])
+    x = first.clone()
+    got = step(x, x[:, :n_q], x[:, -n_q:])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(x[:, n_q:-n_q], first[:, n_q:-n_q])
+    assert q.qe_workspace_status(ws) == q.QE_OK
+
+
 def test_bad_pages_are_masked_and_recorded(q, cuda):
     d = attend_inputs("bf16", 64, 1, 4, 8, 24, [20, 40], seed=4)
     good = d["tb"][1, 2]
