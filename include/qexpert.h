@@ -467,7 +467,8 @@ typedef struct {
  *   pos int32 [n_axes][T] device: positions for the rotation, NULL = kv_pos on
  *     every axis.
  *   kv_pos int32 [T] device: place of token t among its sequence's own tokens;
- *     negative marks a padding row, of which nothing is read or written.
+ *     negative marks a padding row, for which nothing is written.  Its q, k, v
+ *     and pos are read all the same (they have to be there) and do not matter.
  *   seq int32 [T] device: row of `table` of token t, NULL = t.
  *   table int32 [n_seq][table_stride] device: page of tokens
  *     [j * page_size, (j + 1) * page_size) of a sequence at column j.
@@ -500,7 +501,8 @@ QE_API size_t attn_workspace_bytes(const qe_kv_cache* cache, int n_q, int B);
  *     prefix_len = 0.  prefix_len is a host value (a captured graph keeps it).
  *   kv_len int32 [B] device; table int32 [B][table_stride] device.  kv_len 0:
  *     the prefix alone; with no prefix either, out is 0 and lse -inf.
- *     Negative: a padding row, whose out and lse are left as they were.
+ *     Negative: a padding row, whose out and lse are left as they were (its q
+ *     is read and does not matter).
  *   lse fp32 [B][n_q] device or NULL: ln sum_j exp(scale q . k_j).
  * Several query tokens of one sequence are several rows with the same pages
  * and kv_len one apart.  scale is in [0, 2^64].  n_q % n_kv == 0, n_q <= 1024, B <= 4096,

@@ -197,7 +197,9 @@ __global__ void __launch_bounds__(kKvThreads) qe_kv_append_kernel(const __grid_c
     if (second) store8(dst + x.e1, v);
   };
 
-  // the first items are on their way while places and angles are worked out
+  // The first items are on their way while places and angles are worked out.  Padding rows'
+  // are read, too: to wait for kv_pos before costs 0.25 us of 1 token's 3.1 and 1.7 us of
+  // 16384 tokens' 71.1.
   Item x;
   int i = 0, it = threadIdx.x;  // token of the CTA's, item of the token
   auto settle = [&](int& ti, int& k) {

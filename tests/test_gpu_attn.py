@@ -465,6 +465,40 @@ def test_places_of_the_same_rows(q, cuda):
     assert q.qe_workspace_status(ws) == q.QE_OK
 
 
+@pytest.mark.parametrize("T", [5, 3000])
+def test_what_padding_rows_hold_does_not_matter(q, cuda, T):
+    # padding rows of NaN, with positions, sequences and lengths out of any range: the others' results, bit for bit
+    import torch
+    n_q, n_kv, D, page = 4, 2, 64, 8
+    g = torch.Generator(device="cuda").manual_seed(25)
+    x = torch.randn((T, n_q + 2 * n_kv, D), generator=g, device="cuda").to(torch.bfloat16)
+    pad = torch.arange(T, device="cuda") % 3 == 1
+    rope = q.Rope(torch.rand(D // 2, generator=g, device="cuda"))
+    table = torch.arange(T, dtype=torch.int32, device="cuda").reshape(T, 1)
+    got = []
+    for filled in (False, True):
+        y, kv_pos = x.clone(), torch.full((T,), 3, dtype=torch.int32, device="cuda")
+        pos, seq = kv_pos + 100, torch.arange(T, dtype=torch.int32, device="cuda")
+        kv_pos[pad] = -1
+        if filled:
+            y[pad] = NAN
+            kv_pos[pad], pos[pad], seq[pad] = -2147483648, 2147483647, 2147483647
+        kp = torch.zeros((T, n_kv, page, D), dtype=torch.bfloat16, device="cuda")
+        kc = q.KVCache(kp, torch.zeros_like(kp))
+        out, o = torch.full((2, T, n_q, D), 5.0, dtype=torch.bfloat16, device="cuda")
+        ws = q.attn_workspace(kc, n_q, T)
+        q.attn_kv_append(kc, y[:, :n_q], y[:, n_q:n_q + n_kv], y[:, n_q + n_kv:], table, kv_pos, out, rope=rope, pos=pos,
+                         seq=seq, ws=ws)
+        lens = torch.where(pad, kv_pos, 4)
+        pp = torch.zeros(1, dtype=torch.int32, device="cuda")
+        q.attn_decode_step(kc, y[:, :n_q], o, table, lens, pp, 4, ws=ws)  # the prefix's blocks hold all rows
+        assert q.qe_workspace_status(ws) == q.QE_OK
+        assert bool((out[pad] == 5).all()) and bool((o[pad] == 5).all())
+        got.append((out, o, kc.k, kc.v))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert not bool(got[0][1].isnan().any())
+
+
 def test_bad_pages_are_masked_and_recorded(q, cuda):
     d = attend_inputs("bf16", 64, 1, 4, 8, 24, [20, 40], seed=4)
     good = d["tb"][1, 2]
