@@ -293,10 +293,7 @@ struct Row {
   }
 
   // All CTAs of the row, with what they wrote to each other.
-  QE_DEV void sync_all() const {
-    if (STREAM && size == 1) __syncthreads();
-    else cluster_sync();
-  }
+  QE_DEV void sync_all() const { cluster_sync(); }
   // Every CTA's v, by rank, in the returned array (valid until the next but one call).
   QE_DEV const u64* all_gather(u64 v) {
     u64* slots = sh.xch[turn];
