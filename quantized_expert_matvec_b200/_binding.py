@@ -486,6 +486,11 @@ class KVCache:
         self._dev = k.get_device()
 
 
+def _current(cache):
+    if cache._dev != _device():
+        raise ValueError(f"the cache is on cuda:{cache._dev}, the current device is cuda:{_device()}")
+
+
 class Rope:
     """Rotary positions: inv_freq float32 CUDA [rotary_dim / 2]; pair_axis, the
     position axis of each pair (None: axis 0); adjacent pairs (2i, 2i + 1)
@@ -519,6 +524,7 @@ def attn_workspace(cache: KVCache, n_q: int, B: int):
     """Allocate (through torch) and zero a workspace for attn_decode_step with
     B rows of n_q heads; it serves attn_kv_append too."""
     import torch
+    _current(cache)
     ws = torch.empty(attn_workspace_bytes(cache, n_q, B), dtype=torch.uint8, device=cache.k.device)
     qe_workspace_init(ws)
     return ws
@@ -537,8 +543,7 @@ def attn_kv_append(cache: KVCache, q, k, v, table, kv_pos, q_out=None, rope: Rop
         _need("q_out", q_out)
     dev, D, dtype = _device(), cache.head_dim, k.dtype
     i32, T, n_kv = _torch.int32, k.shape[0], cache.n_kv
-    if cache._dev != dev:
-        raise ValueError(f"the cache is on cuda:{cache._dev}, the current device is cuda:{dev}")
+    _current(cache)
     kp, ks = _heads("k", k, dtype, T, n_kv, D, dev)
     vp, vs = _heads("v", v, dtype, T, n_kv, D, dev)
     n_q, qp, qs, op, os_ = 0, None, 0, None, 0
@@ -572,8 +577,7 @@ def attn_decode_step(cache: KVCache, q, out, table, kv_len, prefix_pages=None, p
     dev, D, dtype = _device(), cache.head_dim, cache.dtype
     i32 = _torch.int32
     B, n_q = q.shape[0], q.shape[1]
-    if cache._dev != dev:
-        raise ValueError(f"the cache is on cuda:{cache._dev}, the current device is cuda:{dev}")
+    _current(cache)
     qp, qs = _heads("q", q, dtype, B, n_q, D, dev)
     op, os_ = _heads("out", out, dtype, B, n_q, D, dev)
     rows, cols = table.shape

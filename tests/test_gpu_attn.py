@@ -688,6 +688,25 @@ def test_empty_batch(q, cuda):
     torch.cuda.synchronize()
 
 
+def test_another_current_device_is_refused(q, cuda, monkeypatch):
+    # one GPU is enough: the binding is told that the current device is the next one
+    import torch
+    from quantized_expert_matvec_b200 import _binding
+    d = attend_inputs("bf16", 64, 1, 2, 16, 0, [3], seed=26)
+    kc = q.KVCache(d["kp"], d["vp"])
+    ws, at = q.attn_workspace(kc, 2, 1), torch.zeros(1, dtype=torch.int32, device="cuda")
+    tb, k = torch.from_numpy(d["tb"]).cuda(), d["q"][:, :1]
+    monkeypatch.setattr(_binding, "_device", lambda: 1)
+    with pytest.raises(ValueError, match="cuda:0, the current device is cuda:1"):
+        q.attn_workspace(kc, 2, 1)
+    with pytest.raises(ValueError, match="cuda:0, the current device is cuda:1"):
+        q.attn_kv_append(kc, None, k, k, tb, at, ws=ws)
+    with pytest.raises(ValueError, match="cuda:0, the current device is cuda:1"):
+        q.attn_decode_step(kc, d["q"], torch.empty_like(d["q"]), tb, at, ws=ws)
+    with pytest.raises(ValueError, match="cuda:0, the current device is cuda:1"):
+        q.token_sample(torch.zeros((1, 8), device="cuda"), torch.zeros(1, device="cuda"), at)
+
+
 def test_binding_refuses_before_any_launch(q, cuda):
     import torch
     d = attend_inputs("bf16", 64, 1, 2, 16, 16, [3], seed=14)
