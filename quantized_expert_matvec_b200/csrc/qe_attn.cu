@@ -81,6 +81,9 @@ constexpr int kAttnThreads = 512;  // 8 softmax, 4 producer, product and dealing
 // registers a thread: 256 x 176 + 256 x 80 = 65536 = 512 x 128, the launch's
 constexpr int kSoftRegs = 176, kOtherRegs = 80;
 constexpr int kMaxStages = 10, kSegRing = 6;
+// What a CTA waits at its end for its own copies and products, whatever the callers' limit:
+// they take microseconds.
+constexpr uint64_t kDrainNs = 50 * 1000 * 1000;
 constexpr int kSegReaders = kSoftWarps + kProdWarps + 1;
 
 template <int D>
@@ -328,22 +331,24 @@ struct Shared {
 
 static_assert(sizeof(Shared) <= 2048, "beside the dynamic shared memory");
 
-// Bounded wait.  Once one has given up, the error is recorded, `abort` is set and
-// every later wait returns at once: the roles walk to their ends (within the same
-// bounds of memory) and the CTA leaves in the ordinary way.
-QE_DEV void wait_for(uint64_t* bar, uint32_t parity, Shared& sh, const AttnArgs& a) {
+// Bounded wait; false if it gave up.  Once one has, the error is recorded, `abort` is set and
+// every later wait that is not over returns at once: the producers and the dealer write nothing
+// any more, the roles walk to the end of their segment (within the same bounds of memory) and
+// the CTA leaves in the ordinary way.
+QE_DEV bool wait_for(uint64_t* bar, uint32_t parity, Shared& sh, const AttnArgs& a) {
   uint64_t deadline = 0;
   for (int i = 0; !mbar_try_wait(bar, parity); ++i) {
-    if (*(volatile int*)&sh.abort) return;
+    if (*(volatile int*)&sh.abort) return false;
     if ((i & 15) != 15) continue;  // the timer is slow to read
     const uint64_t now = gtimer();
     if (deadline == 0) deadline = now + a.budget_ns;
     if (now > deadline) {
       *(volatile int*)&sh.abort = 1;
       set_error(a.err, QE_ERR_TIMEOUT);
-      return;
+      return false;
     }
   }
+  return true;
 }
 // The k-th completion (from 0) of a barrier that is one of two used in turn.  A wait
 // sees one bit of the phase: whoever waits for completion k has to know already that
@@ -371,13 +376,13 @@ QE_DEV void group_sync(int group) {
 struct Reader {
   int at = 0;
   uint32_t phase = 0;
-  // Copies the next segment; by every lane of a warp, or by one thread alone.
-  QE_DEV void next(Segment& x, Shared& sh, const AttnArgs& a, bool warp, bool one) {
-    wait_for(&sh.seg_full[at], phase, sh, a);
+  // Copies the next segment, by every lane of a warp.  The lanes agree on its end: one may have
+  // seen a wait give up where another has not.
+  QE_DEV void next(Segment& x, Shared& sh, const AttnArgs& a) {
+    const bool there = wait_for(&sh.seg_full[at], phase, sh, a);
     x = sh.seg[at];
-    if (*(volatile int*)&sh.abort) x.n = 0;  // the ring may hold anything now
-    if (warp) __syncwarp();
-    if (one) mbar_arrive(&sh.seg_empty[at]);
+    if (!__all_sync(0xffffffffu, there && !*(volatile int*)&sh.abort)) x.n = 0;
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.seg_empty[at]);
     if (++at == kSegRing) {
       at = 0;
       phase ^= 1;
@@ -394,7 +399,7 @@ QE_DEV void deal_out(const AttnArgs& a, const Deal& d, long long t, long long t1
   int at = 0;
   uint32_t phase = 1;
   auto put = [&](const Segment& x) {
-    wait_for(&sh.seg_empty[at], phase, sh, a);
+    if (!wait_for(&sh.seg_empty[at], phase, sh, a)) return;  // it may be being read still
     sh.seg[at] = x;
     mbar_arrive(&sh.seg_full[at]);
     if (++at == kSegRing) {
@@ -513,8 +518,10 @@ QE_DEV void produce(const AttnArgs& a, const CUtensorMap* k_map, const CUtensorM
     for (int p = 0; p < Sh::kParts; ++p) {
       const unsigned long long row = (is_v ? v_row : k_row) + 2 * p * Sh::kDims;
       const uint32_t lv = is_v ? v_live : live;
-      wait_for(&sh.empty[stage], phase, sh, a);
-      __syncwarp();
+      // Once a wait has given up nothing more is copied: copies into a stage that is still being
+      // filled would take its barrier's counts beyond their range.  The lanes go together.
+      const bool given_up = *(volatile int*)&sh.abort;
+      if (!__all_sync(0xffffffffu, wait_for(&sh.empty[stage], phase, sh, a) && !given_up)) return;
       const uint32_t at = stage * Sh::kStage;
       if (lv == 0xffffffffu && a.run_bits >= 3) {
         // lane l: run l mod (32 / run) of the warp's rows, 64 dims l / (32 / run)
@@ -555,7 +562,7 @@ QE_DEV void produce(const AttnArgs& a, const CUtensorMap* k_map, const CUtensorM
   while (true) {
     bool first = false, v_first = false;
     if (left == 0) {
-      reader.next(x, sh, a, true, lane == 0);
+      reader.next(x, sh, a);
       left = x.n;
       key0 = x.key0;
       more = left > 0;
@@ -619,12 +626,12 @@ QE_DEV void produce(const AttnArgs& a, const CUtensorMap* k_map, const CUtensorM
     ++n;
   }
   cp_async_wait_all();
-  // nothing may be in flight when the CTA leaves (after a wait that gave up, the last stages could be)
-  for (int i = max(0, issued - Sh::kStages); i < issued; ++i) {
-    const uint64_t deadline = gtimer() + a.budget_ns;
+  // nothing may be in flight when the CTA leaves (after a wait that gave up, the last stages could be,
+  // and one that not all warps have filled does not complete: it is given the time)
+  const uint64_t deadline = gtimer() + kDrainNs;
+  for (int i = max(0, issued - Sh::kStages); i < issued; ++i)
     while (!mbar_try_wait(&sh.full[i % Sh::kStages], (i / Sh::kStages) & 1))
       if (gtimer() > deadline) break;
-  }
 }
 
 // One warp, every value in it uniform.
@@ -704,7 +711,7 @@ QE_DEV void multiply(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigne
   Reader reader;
   Segment x;
   auto next_segment = [&](Segment& y) {
-    reader.next(y, sh, a, true, (threadIdx.x & 31) == 0);
+    reader.next(y, sh, a);
     y.n = uniform(y.n);
     y.rows = uniform(y.rows);
   };
@@ -780,7 +787,7 @@ QE_DEV void multiply(const AttnArgs& a, Shared& sh, unsigned char* ring, unsigne
   // whatever happened, nothing is in flight when this returns
   __syncwarp();
   mma_commit(&sh.drained);
-  const uint64_t deadline = gtimer() + a.budget_ns;
+  const uint64_t deadline = gtimer() + kDrainNs;
   while (!mbar_try_wait_sleep(&sh.drained, 0, 10000u))
     if (gtimer() > deadline) {
       set_error(a.err, QE_ERR_TIMEOUT);
@@ -1083,7 +1090,7 @@ QE_DEV void soften(const AttnArgs& a, Shared& sh, unsigned char* ps, uint32_t tm
   int n = 0, own_n = 0, wide_n = 0, tile = 0;
 #pragma unroll 1
   for (int seg = 0;; ++seg) {
-    reader.next(x, sh, a, true, lane == 0);
+    reader.next(x, sh, a);
     // a group's warps have to go through the same barriers: they end together
     if (group_vote(group, x.n == 0)) break;
     if (x.rows > kNarrow) {

@@ -677,6 +677,29 @@ def test_queries_that_arrive_after_the_keys(q, cuda, D, G, prefix, lens):
     assert q.qe_workspace_status(ws) == q.QE_OK
 
 
+def test_a_wait_that_gives_up_leaves_the_gpu_usable(q, cuda):
+    # a limit of a microsecond, which waits for memory can pass: whatever such calls return, the status says
+    # whether it counts, and the calls after them are right
+    import torch
+    ds = [attend_inputs("bf16", 128, 2, 4, 16, 3000, [700, 0, 90] * 20, seed=27),
+          attend_inputs("f16", 256, 1, 16, 64, 500, [4000, 3], seed=28), attend_inputs("bf16", 64, 4, 4, 5, 0, [300] * 70, seed=29)]
+    want = [run_attend(q, d) for d in ds]
+    try:
+        q.qe_set_wait_budget_ns(1000)
+        for trial in range(5):
+            for d, (out, lse, ws) in zip(ds, want):
+                got, lse2, _ = run_attend(q, d, ws=ws)
+                status = q.qe_workspace_status(ws)
+                assert status in (q.QE_OK, q.QE_ERR_TIMEOUT)
+                assert status != q.QE_OK or (torch.equal(got, out) and torch.equal(lse2, lse))
+    finally:
+        q.qe_set_wait_budget_ns(200_000_000)
+    for d, (out, lse, ws) in zip(ds, want):
+        got, lse2, _ = run_attend(q, d, ws=ws)
+        assert q.qe_workspace_status(ws) == q.QE_OK
+        assert torch.equal(got, out) and torch.equal(lse2, lse)
+
+
 def test_empty_batch(q, cuda):
     import torch
     d = attend_inputs("bf16", 64, 1, 2, 16, 0, [3], seed=13)
