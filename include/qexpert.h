@@ -505,14 +505,17 @@ QE_API size_t attn_workspace_bytes(const qe_kv_cache* cache, int n_q, int B);
  *     is read and does not matter).
  *   lse fp32 [B][n_q] device or NULL: ln sum_j exp(scale q . k_j).
  * Several query tokens of one sequence are several rows with the same pages
- * and kv_len one apart.  scale is in [0, 2^64].  n_q % n_kv == 0, n_q <= 1024, B <= 4096,
- * table_stride * page_size and prefix_len < 2^30.  Scores, softmax statistics
- * and sums are fp32; the softmax numerators are rounded to the cache's dtype
- * for the product with v.  A kv_len beyond the table is cut to it, a key on a
- * page out of range counts as masked, and either records QE_ERR_INVALID_ARG in
- * the workspace; a bounded wait that gives up records QE_ERR_TIMEOUT there (out is
- * then not to be used).  The result does not depend on the order in which the
- * GPU runs the parts.  Two launches.  Calls that share a workspace must be ordered on the device. */
+ * and kv_len one apart.  scale is in [0, 2^64].  n_q % n_kv == 0, n_q <= 1024,
+ * B <= 4096, table_stride * page_size and prefix_len < 2^30.  Scores, softmax
+ * statistics and sums are fp32; the softmax numerators are rounded to the
+ * cache's dtype for the product with v (fp16: those below 2^-32 of the largest
+ * are 0).  A kv_len beyond the table is cut to it, a key on a page out of range
+ * counts as masked, and either records QE_ERR_INVALID_ARG in the workspace; a
+ * bounded wait that gives up records QE_ERR_TIMEOUT there (out is then not to be
+ * used).  The waits' limit is qe_set_wait_budget_ns's and 10 us for each tile of
+ * 128 keys that a multiprocessor can get by the shapes.  The result does not
+ * depend on the order in which the GPU runs the parts.  Two launches.  Calls
+ * that share a workspace must be ordered on the device. */
 QE_API int attn_decode_step(const qe_kv_cache* cache, int B, int n_q, const void* q, int64_t q_stride,
                             const int32_t* prefix_pages, int prefix_len, const int32_t* table, int table_stride,
                             const int32_t* kv_len, float scale, void* out, int64_t out_stride, float* lse,

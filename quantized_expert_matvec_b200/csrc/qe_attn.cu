@@ -81,6 +81,8 @@ constexpr int kAttnThreads = 512;  // 8 softmax, 4 producer, product and dealing
 // registers a thread: 256 x 176 + 256 x 80 = 65536 = 512 x 128, the launch's
 constexpr int kSoftRegs = 176, kOtherRegs = 80;
 constexpr int kMaxStages = 10, kSegRing = 6;
+// A wait's limit grows by this for each tile of a CTA: a tile takes 1.3 to 2.4 us.
+constexpr uint64_t kTileNs = 10 * 1000;
 // What a CTA waits at its end for its own copies and products, whatever the callers' limit:
 // they take microseconds.
 constexpr uint64_t kDrainNs = 50 * 1000 * 1000;
@@ -1503,7 +1505,6 @@ extern "C" QE_API int attn_decode_step(const qe_kv_cache* c, int B, int n_q, con
   a.prefix_groups = (int2*)(w + p.off_groups);
   a.ml_prefix = (float2*)(w + p.off_mlp); a.ml_own = (float2*)(w + p.off_mlo);
   a.part_prefix = (float*)(w + p.off_pp); a.part_own = (float*)(w + p.off_po);
-  a.budget_ns = wait_budget_ns();
   a.B = B; a.n_q = n_q; a.n_kv = c->n_kv; a.G = n_q / c->n_kv; a.n_pages = c->n_pages;
   a.table_stride = table_stride; a.prefix_len = prefix_len;
   a.prefix_tiles = (prefix_len + kTile - 1) / kTile;
@@ -1517,6 +1518,13 @@ extern "C" QE_API int attn_decode_step(const qe_kv_cache* c, int B, int n_q, con
   a.group = fast_div((uint32_t)a.G);
   // a wide tile of two blocks of 128 rows takes about twice a narrow one's time
   a.prefix_cost = (long long)B * a.G > 128 && p.max_rows > 128 ? 2 : 1;
+  // A role may have to wait for as long as another's segment takes (a softmax group without rows
+  // for a whole prefix), so the limit grows with the tiles that one CTA can have.
+  const long long prefix_ctas = line == 0 ? 0 : p.rb_prefix <= p.grid ? (long long)a.groups * p.rb_prefix : p.grid;
+  const long long cap = (long long)table_stride * c->page_size, own = (long long)B * c->n_kv * p.rb_own * (cap / kTile + 2);
+  const long long tiles = (line == 0 ? 0 : p.rb_prefix <= p.grid ? line / a.groups + 1 : line * (p.rb_prefix / p.grid + 1)) +
+                          own / (prefix_ctas < p.grid ? p.grid - prefix_ctas : p.grid) + 1;
+  a.budget_ns = wait_budget_ns() + (unsigned long long)tiles * a.prefix_cost * kTileNs;
   CacheMaps m{};
   int bits = 0;
   while (bits < 5 && !((c->page_size >> bits) & 1)) ++bits;

@@ -700,6 +700,35 @@ def test_a_wait_that_gives_up_leaves_the_gpu_usable(q, cuda):
         assert torch.equal(got, out) and torch.equal(lse2, lse)
 
 
+def test_segments_longer_than_the_limit(q, cuda):
+    # 128 rows of head_dim 256 are one softmax group's: the other waits for all of a prefix of 90 tiles a
+    # multiprocessor, some hundred microseconds, for its first own keys.  That is no reason to give up
+    import torch
+    d = attend_inputs("bf16", 256, 1, 8, 64, 640, [300, 1, 0, 129] * 4, seed=30)
+    d["pp"], d["prefix"] = np.tile(d["pp"], 2700), 2700 * 640
+    want, lse, ws = run_attend(q, d)
+    assert q.qe_workspace_status(ws) == q.QE_OK
+    try:
+        q.qe_set_wait_budget_ns(20_000)
+        got, lse2, _ = run_attend(q, d, ws=ws)
+        assert q.qe_workspace_status(ws) == q.QE_OK
+    finally:
+        q.qe_set_wait_budget_ns(200_000_000)
+    assert torch.equal(got, want) and torch.equal(lse2, lse)
+    # the prefix's keys are 640 keys 2700 times: as those 640 with ln 2700 more in their scores
+    kp, vp, qq = host(d["kp"]), host(d["vp"]), host(d["q"])
+    for b in (0, 2, 7):
+        k, v = (np.concatenate([ref.gather(p, 64, d["pp"], 640, 0), ref.gather(p, 64, d["tb"][b], d["lens"][b], 0)])
+                for p in (kp, vp))
+        s = d["scale"] * (qq[b] @ k.T)
+        s[:, :640] += math.log(2700)
+        p = np.exp(s - s.max(axis=1, keepdims=True))
+        o = p @ v / p.sum(axis=1, keepdims=True)
+        # numerators' and results' roundings to bf16, and the score's and the sums' in fp32
+        tol = (2 * ref.HALF_STEP["bf16"] + 2.0 ** -9) * (p @ np.abs(v)) / p.sum(axis=1, keepdims=True)
+        assert np.all(np.abs(host(got)[b] - o) <= tol)
+
+
 def test_empty_batch(q, cuda):
     import torch
     d = attend_inputs("bf16", 64, 1, 2, 16, 0, [3], seed=13)
