@@ -557,6 +557,8 @@ def attn_kv_append(cache: KVCache, q, k, v, table, kv_pos, q_out=None, rope: Rop
         axes = rope.n_axes
         if rope.inv_freq.get_device() != dev:
             _placed("inv_freq", rope.inv_freq, None, dev)
+    if pos is not None and pos.dim() > 1 and pos.shape[0] != axes:
+        raise ValueError(f"pos must be [{axes}, {T}], got {tuple(pos.shape)}")
     rc = lib.attn_kv_append(cache._ref, rope._ref if rope is not None else None, T, n_q, qp, kp, vp, _code(dtype), qs, ks,
                             vs, op, os_, _vec("pos", pos, i32, axes * T, dev), _vec("kv_pos", kv_pos, i32, T, dev),
                             _vec("seq", seq, i32, T, dev), _vec("table", table, i32, None, dev), n_seq, cols,
@@ -585,6 +587,8 @@ def attn_decode_step(cache: KVCache, q, out, table, kv_len, prefix_pages=None, p
         raise ValueError(f"table must have {B} rows, got {rows}")
     if prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() * cache.page_size < prefix_len):
         raise ValueError("prefix_pages must hold prefix_len tokens")
+    if lse is not None and lse.dim() > 1 and lse.shape[0] != B:
+        raise ValueError(f"lse must be [{B}, {n_q}], got {tuple(lse.shape)}")
     rc = lib.attn_decode_step(cache._ref, B, n_q, qp, qs, _vec("prefix_pages", prefix_pages, i32, None, dev), prefix_len,
                               _vec("table", table, i32, None, dev), cols, _vec("kv_len", kv_len, i32, B, dev),
                               D ** -0.5 if scale is None else scale, op, os_,

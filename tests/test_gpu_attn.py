@@ -759,6 +759,26 @@ def test_another_current_device_is_refused(q, cuda, monkeypatch):
         q.token_sample(torch.zeros((1, 8), device="cuda"), torch.zeros(1, device="cuda"), at)
 
 
+def test_transposed_arguments_are_refused(q, cuda):
+    # as many elements as wanted, in another order
+    import torch
+    d = attend_inputs("bf16", 64, 1, 2, 16, 0, [3, 4, 5], seed=31)
+    kc = q.KVCache(d["kp"], d["vp"])
+    ws, at = q.attn_workspace(kc, 2, 3), torch.zeros(3, dtype=torch.int32, device="cuda")
+    tb, k = torch.from_numpy(d["tb"]).cuda(), d["q"][:, :1]
+    rope = q.Rope(torch.rand(32, device="cuda"), [0, 1] * 16)
+    pos = torch.zeros((2, 3), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match=r"pos must be \[2, 3\]"):
+        q.attn_kv_append(kc, None, k, k, tb, at, rope=rope, pos=pos.t().contiguous(), ws=ws)
+    q.attn_kv_append(kc, None, k, k, tb, at, rope=rope, pos=pos, ws=ws)
+    q.attn_kv_append(kc, None, k, k, tb, at, rope=rope, pos=pos.flatten(), ws=ws)
+    lse, out = torch.zeros((3, 2), device="cuda"), torch.empty_like(d["q"])
+    with pytest.raises(ValueError, match=r"lse must be \[3, 2\]"):
+        q.attn_decode_step(kc, d["q"], out, tb, at + 1, lse=lse.t().contiguous(), ws=ws)
+    q.attn_decode_step(kc, d["q"], out, tb, at + 1, lse=lse, ws=ws)
+    assert q.qe_workspace_status(ws) == q.QE_OK
+
+
 def test_binding_refuses_before_any_launch(q, cuda):
     import torch
     d = attend_inputs("bf16", 64, 1, 2, 16, 16, [3], seed=14)
