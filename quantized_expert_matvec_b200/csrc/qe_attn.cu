@@ -35,12 +35,13 @@
 //         (each role working them out for itself made the code 160 KB and every
 //         role wait for its instructions).
 // Measured (device time of both kernels): 128 rows behind 32768 shared keys of 8 heads of
-// 128 192 us, 363 TFLOP/s; 61 ragged rows of up to 8192 keys 45 us, 2.7 TB/s; two
-// sequences of 65535 and 131071 keys of 2 heads of 256 82 us, 4.9 TB/s; one sequence of 4093 keys 15
+// 128 198 us, 353 TFLOP/s; 61 ragged rows of up to 8192 keys 47 us, 2.6 TB/s; two
+// sequences of 65535 and 131071 keys of 2 heads of 256 82 us, 4.9 TB/s; one sequence of 4093 keys 16
 // us.  Without the exponentials, with an eighth of the products or without most of the
-// copies each of these stays within a tenth: what bounds a tile is the hand-over from one
-// role to the next (producers, scores, softmax, outputs), it seems: about 2.4 us a wide tile and
-// 1.3 us a narrow one, and 8 us before the first.
+// copies each of these stays within a tenth: none of them bounds a tile by itself.  What
+// remains are the hand-overs from one role to the next (producers, scores, softmax,
+// outputs), not timed by themselves: about 2.4 us a wide tile and 1.3 us a narrow one,
+// and 8 us before the first.
 // The reference m need not be the maximum (for fp16 it is set 7 below it): it is raised,
 // and o and l rescaled, only when a score passes the maximum that it was set by by more
 // than 2^8.  l is the sum of the fp32 numerators; their rounding to the cache's dtype is

@@ -8,7 +8,7 @@
 // angles of a token's rotary_dim / 2 pairs are computed once, into shared memory, and
 // used by all its heads.  A thread's item is 16 elements of a head in two runs of 8:
 // two 16-byte loads (four for fp32) and two 16-byte stores, requested an item ahead.
-// Measured: 1 token of 48 heads of 128 2.8 us, 256 tokens 3.7 us, 16384 tokens (403 MB)
+// Measured: 1 token of 48 heads of 128 3.1 us, 256 tokens 3.7 us, 16384 tokens (403 MB)
 // 71 us, 5.7 TB/s (with a thread's 16 elements in one run, which leaves its neighbours'
 // requests half a sector each, 79 us).
 #include <cuda_bf16.h>

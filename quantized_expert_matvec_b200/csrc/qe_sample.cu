@@ -19,8 +19,8 @@
 // consecutive 16-byte pieces, so that threads are in index order (which the
 // running sums need) and their 16-byte reads fall on different banks.  Many rows
 // (STREAM): the shared memory would leave few rows at work at a time (18 of 800 KB),
-// so that four CTAs a row read it from global memory, mostly the L2 cache, in
-// every pass, each warp a run of its own, and 74 rows are at work.  Measured at 256 rows of
+// so that four CTAs a row (eight for more than 262144 logits) read it from global memory,
+// mostly the L2 cache, in every pass, each warp a run of its own, and 74 rows are at work.  Measured at 256 rows of
 // 200000 fp32 logits: 443 us from shared memory (16 CTAs a row), streamed by 1, 2, 4
 // and 8 CTAs a row 388, 268, 250 and 301 us; at 64 rows of 100003 bf16 logits 64 us and
 // (by 4) 85 us.
