@@ -449,11 +449,6 @@ def _heads(name, t, dtype, T, heads, dim, dev):
     return t.data_ptr(), s[0]
 
 
-def _need(name, t):
-    if t is None:
-        raise ValueError(f"{name} is missing")
-
-
 def _on(stream, dev):
     return _raw_stream(dev) if stream is None else _stream(stream)
 
@@ -486,9 +481,9 @@ class KVCache:
         self._dev = k.get_device()
 
 
-def _current(cache):
-    if cache._dev != _device():
-        raise ValueError(f"the cache is on cuda:{cache._dev}, the current device is cuda:{_device()}")
+def _current(cache, dev):
+    if cache._dev != dev:
+        raise ValueError(f"the cache is on cuda:{cache._dev}, the current device is cuda:{dev}")
 
 
 class Rope:
@@ -524,7 +519,7 @@ def attn_workspace(cache: KVCache, n_q: int, B: int):
     """Allocate (through torch) and zero a workspace for attn_decode_step with
     B rows of n_q heads; it serves attn_kv_append too."""
     import torch
-    _current(cache)
+    _current(cache, _device())
     ws = torch.empty(attn_workspace_bytes(cache, n_q, B), dtype=torch.uint8, device=cache.k.device)
     qe_workspace_init(ws)
     return ws
@@ -538,12 +533,11 @@ def attn_kv_append(cache: KVCache, q, k, v, table, kv_pos, q_out=None, rope: Rop
     t).  pos int32 [n_axes, T] are the rotation's positions (None: kv_pos).  q may
     be None, else q_out is needed; q_out may be q itself where the dtypes agree.
     ws: any workspace."""
-    _need("ws", ws)
-    if q is not None:
-        _need("q_out", q_out)
+    if ws is None or (q_out is None and q is not None):
+        raise ValueError(f"{'ws' if ws is None else 'q_out'} is missing")
     dev, D, dtype = _device(), cache.head_dim, k.dtype
     i32, T, n_kv = _torch.int32, k.shape[0], cache.n_kv
-    _current(cache)
+    _current(cache, dev)
     kp, ks = _heads("k", k, dtype, T, n_kv, D, dev)
     vp, vs = _heads("v", v, dtype, T, n_kv, D, dev)
     n_q, qp, qs, op, os_ = 0, None, 0, None, 0
@@ -557,7 +551,7 @@ def attn_kv_append(cache: KVCache, q, k, v, table, kv_pos, q_out=None, rope: Rop
         axes = rope.n_axes
         if rope.inv_freq.get_device() != dev:
             _placed("inv_freq", rope.inv_freq, None, dev)
-    if pos is not None and pos.dim() > 1 and pos.shape[0] != axes:
+    if axes > 1 and pos is not None and pos.shape[0] != axes and pos.dim() > 1:
         raise ValueError(f"pos must be [{axes}, {T}], got {tuple(pos.shape)}")
     rc = lib.attn_kv_append(cache._ref, rope._ref if rope is not None else None, T, n_q, qp, kp, vp, _code(dtype), qs, ks,
                             vs, op, os_, _vec("pos", pos, i32, axes * T, dev), _vec("kv_pos", kv_pos, i32, T, dev),
@@ -575,11 +569,12 @@ def attn_decode_step(cache: KVCache, q, out, table, kv_len, prefix_pages=None, p
     as it was), into out.  scale defaults to head_dim ** -0.5; lse float32
     [B, n_q] receives the logarithm of the softmax's denominator; ws is
     attn_workspace's."""
-    _need("ws", ws)
+    if ws is None:
+        raise ValueError("ws is missing")
     dev, D, dtype = _device(), cache.head_dim, cache.dtype
     i32 = _torch.int32
     B, n_q = q.shape[0], q.shape[1]
-    _current(cache)
+    _current(cache, dev)
     qp, qs = _heads("q", q, dtype, B, n_q, D, dev)
     op, os_ = _heads("out", out, dtype, B, n_q, D, dev)
     rows, cols = table.shape
@@ -587,7 +582,7 @@ def attn_decode_step(cache: KVCache, q, out, table, kv_len, prefix_pages=None, p
         raise ValueError(f"table must have {B} rows, got {rows}")
     if prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() * cache.page_size < prefix_len):
         raise ValueError("prefix_pages must hold prefix_len tokens")
-    if lse is not None and lse.dim() > 1 and lse.shape[0] != B:
+    if lse is not None and lse.shape[0] != B and lse.dim() > 1:
         raise ValueError(f"lse must be [{B}, {n_q}], got {tuple(lse.shape)}")
     rc = lib.attn_decode_step(cache._ref, B, n_q, qp, qs, _vec("prefix_pages", prefix_pages, i32, None, dev), prefix_len,
                               _vec("table", table, i32, None, dev), cols, _vec("kv_len", kv_len, i32, B, dev),
