@@ -385,6 +385,7 @@ struct Reader {
     const bool there = wait_for(&sh.seg_full[at], phase, sh, a);
     x = sh.seg[at];
     if (!__all_sync(0xffffffffu, there && !*(volatile int*)&sh.abort)) x.n = 0;
+    __syncwarp();  // all lanes have read it before its place is given back (a vote orders no memory)
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.seg_empty[at]);
     if (++at == kSegRing) {
       at = 0;
